@@ -95,9 +95,11 @@ def draw(rng):
                       rng.choice([0.5, 1.0, 2.0]))
     if op == "router_grad":
         E = rng.choice([8, 21, 64, 100, 256, 384])
-        return _router_grad(_log(rng, 1, 4096), E, rng.randint(1, min(8, E)),
-                            8 * _log(rng, 8, 896), rng.choice(["softmax", "sigmoid"]),
-                            rng.random() < 0.6, rng.choice([1.0, 2.5]))
+        k = rng.randint(1, min(8, E))
+        # one renormalised gate is constant: its gradient is rounding noise around zero
+        return _router_grad(_log(rng, 1, 4096), E, k, 8 * _log(rng, 8, 896),
+                            rng.choice(["softmax", "sigmoid"]), k > 1 and rng.random() < 0.6,
+                            rng.choice([1.0, 2.5]))
     E = rng.randint(3, 48)
     k = rng.randint(1, min(8, E))
     T = _log(rng, 1, 4096)
