@@ -311,6 +311,157 @@ moe_status moe_ep_regroup(const int32_t* counts, int32_t W, int32_t E_loc, int64
                           int32_t* num_active, int32_t* chunk_offsets, int32_t* num_chunks,
                           void* stream);
 
+/* Score functions of moe_route_scored. */
+enum { MOE_SCORE_SOFTMAX = 1, MOE_SCORE_SIGMOID = 2 };
+
+/* How moe_route_scored turns logits into a selection and gates. */
+typedef struct moe_router {
+  int32_t score;        /* MOE_SCORE_*: s = softmax over all E logits, or the logistic function of each */
+  int32_t groups;       /* G expert groups of E / G consecutive experts; 1 <= G <= 32, E % G == 0 */
+  int32_t topk_groups;  /* groups a token may choose from, 1..G; k <= topk_groups * (E / G) */
+  int32_t group_top;    /* a group's score: the sum of its 1 or 2 largest keys */
+  int32_t renorm;       /* 1: gates are divided by the sum of the k selected scores; 0: not */
+  float scale;          /* factor of every gate, finite */
+} moe_router;
+
+/*
+ * moe_route_scored -- moe_route_permute with the router of layers that are
+ * trained for balance: scores over all experts, a bias that steers the
+ * selection only, expert groups, and gates from the scores. For token t:
+ *   s[e]   = softmax(logits[t])[e] or 1 / (1 + exp(-logits[t][e]))
+ *   key[e] = s[e] + bias[e]                     (bias NULL: s[e])
+ *   group score = sum of the group_top largest keys of the group (of all
+ *            its keys when it holds fewer); the topk_groups best groups stay
+ *   topk_idx[t] = the k largest keys of those groups, descending
+ *   gates[t][j] = scale * s_j / sum of the k selected s (renorm), or scale * s_j
+ * Equal keys and equal groups go to the lower id. Keys are compared as if in
+ * 64 bits (without a bias, by the logits themselves, which have the same
+ * order). An expert whose logit is NaN or -inf, or whose key is NaN or -inf,
+ * is masked: its score is 0 and it is chosen only when fewer than k experts of
+ * the kept groups are left (in ascending id, gate 0); a masked key adds
+ * nothing to its group's score, and a group of masked experts ranks last. A token whose selected scores sum
+ * to 0 gets gates 0.
+ * The k experts of a token are always distinct. All other arguments, outputs
+ * and limits are those of moe_route_permute, the workspace size included.
+ */
+moe_status moe_route_scored(const float* logits, const float* bias, const void* x, int64_t T,
+                            int32_t E, int32_t k, int64_t d, const moe_router* router,
+                            int32_t chunk_size, int32_t* topk_idx, float* gates,
+                            int32_t* expert_offsets, int32_t* active, int32_t* num_active,
+                            int32_t* chunk_offsets, int32_t* num_chunks, int32_t* perm_token,
+                            int32_t* inv_perm, void* x_perm, void* ws, size_t* ws_bytes,
+                            void* stream);
+
+/*
+ * moe_route_scored_bwd -- gradient of the gates with respect to the logits.
+ * The selection and the bias get none (the selection is piecewise constant).
+ *  d_gates   [T][k] fp32, topk_idx [T][k] int32 as moe_route_scored wrote it
+ *            (an id outside [0, E) contributes nothing), logits [T][E] fp32.
+ *  d_logits  [T][E] fp32, every entry written.
+ * With c = scale, s the scores, S the sum of the k selected ones:
+ *   ds_j = c * d_gates_j, or with renorm c * (d_gates_j - sum_i d_gates_i s_i / S) / S
+ *   sigmoid: d_logits_j = ds_j s_j (1 - s_j), other experts 0
+ *   softmax: d_logits_e = s_e (ds_e - sum_j ds_j s_j)  (ds_e = 0 when not selected)
+ * Masked experts get 0, and so does a token with S == 0. Requires T >= 1,
+ * 1 <= E <= 1024, 1 <= k <= min(E, 32). Only score, renorm and scale of
+ * `router` are read.
+ */
+moe_status moe_route_scored_bwd(const float* d_gates, const float* logits, const int32_t* topk_idx,
+                                int64_t T, int32_t E, int32_t k, const moe_router* router,
+                                float* d_logits, void* stream);
+
+/*
+ * moe_combine_bwd -- backward of moe_unpermute_combine (mode 0) with respect
+ * to the per-slot rows and the gates, in one pass over dy and rows:
+ *   d_rows[inv_perm[t*k+j]] = bf16(gates[t][j] * dy[t])   (as mode 1 writes it)
+ *   d_gates[t][j] = sum_c dy[t][c] * rows[inv_perm[t*k+j]][c]   (fp32, fixed order)
+ *  dy [T][D], rows and d_rows [T*k][D] bf16; d_rows must not overlap rows or
+ *  dy. gates NULL: all ones. D % 8 == 0, 1 <= k <= 32.
+ */
+moe_status moe_combine_bwd(const void* dy, const void* rows, const int32_t* inv_perm,
+                           const float* gates, int64_t T, int32_t k, int64_t D, void* d_rows,
+                           float* d_gates, void* stream);
+
+/*
+ * FP8 rows and weights.
+ *  - FP8 rows: e4m3 [M][K] with one fp32 scale per 1 x 128 block, stored
+ *    group-major: scales[b][m], b < ceil(K/128). The library writes powers of
+ *    two, the smallest 2^e >= 2^-126 with amax <= 448 * 2^e (1 for a block of
+ *    zeros), so that quantizing rounds once; it reads any fp32 scale.
+ *  - FP8 weights (moe_fp8_weight): e4m3 [E][N][K] with one fp32 scale per
+ *    128 x 128 block, scales[e][ceil(N/128)][ceil(K/128)], any fp32 value.
+ *  - 8-bit checkpoint of saved activations: e4m3 [M][C] with one E8M0 scale
+ *    2^(X-127) per 32 elements, uint8 scales[C/32][M], X chosen by the same rule.
+ * e4m3 has no infinity: what is not finite becomes NaN, and the other
+ * elements of its block are quantized as if it were 0.
+ */
+typedef struct moe_fp8_weight {
+  const void* q;        /* device, e4m3 [E][N][K] */
+  const float* scales;  /* device, fp32 [E][ceil(N/128)][ceil(K/128)] */
+  int32_t E, N, K;      /* N % 16 == 0, K % 16 == 0, 1 <= E <= 1024 */
+} moe_fp8_weight;
+
+/* Scale blocks of moe_dequantize_fp8_rows. */
+enum { MOE_FP8_BLOCK128_F32 = 1, MOE_FP8_BLOCK32_E8M0 = 2 };
+
+/*
+ * moe_quantize_fp8_rows -- BF16 rows [T][K] to FP8 rows. With inv_perm (device
+ * int32 [T*k]), token t is quantized once and written to its k permuted rows
+ * inv_perm[t*k+j], which gives the grouped GEMM its input in expert order (M =
+ * T*k); entries outside [0, T*k) are skipped. Without it row t goes to row t
+ * (k must be 1, M = T).
+ *  q [M][K] e4m3, scales [ceil(K/128)][M] fp32. K % 16 == 0, 1 <= k <= 32.
+ */
+moe_status moe_quantize_fp8_rows(const void* x, int64_t T, int64_t K, const int32_t* inv_perm,
+                                 int32_t k, void* q, float* scales, void* stream);
+
+/*
+ * moe_dequantize_fp8_rows -- out [M][K] bf16 = q * scale (one rounding; exact
+ * for the power-of-two scales that the library writes). fmt = MOE_FP8_*: 1 x
+ * 128 blocks with fp32 scales, or 1 x 32 blocks with E8M0 scales (X = 255 is
+ * NaN). K % 16 == 0.
+ */
+moe_status moe_dequantize_fp8_rows(const void* q, const void* scales, int64_t M, int64_t K,
+                                   int32_t fmt, void* out, void* stream);
+
+/*
+ * moe_grouped_fp8_gemm_fwd -- grouped product of FP8 rows with FP8 expert
+ * weights: for every row p of expert e,
+ *   acc[p][n] = sum_b a_scales[b][p] * w.scales[e][n/128][b] *
+ *               sum_{k in block b} a[p][k] * w.q[e][n][k]
+ * (each 128-long partial sum on the tensor cores in fp32, the scaled sum over
+ * the blocks in fp32, in ascending b, so a row's bits do not depend on the
+ * rest of the batch).
+ *  a, a_scales  FP8 rows [M][K] in expert order (moe_quantize_fp8_rows).
+ *  g            groups, g->E == w->E, off[E] == M.
+ *  epi   MOE_EPI_NONE: out bf16 [M][N]; out_scales, saved and saved_scales NULL.
+ *        MOE_EPI_SWIGLU (N % 256 == 0; rows 0..N/2-1 of W[e] are the gate):
+ *        out, out_scales = FP8 rows of silu(acc[:, :N/2]) * acc[:, N/2:], the
+ *        input of the down product; saved, saved_scales: NULL, or the 8-bit
+ *        checkpoint of acc, e4m3 [M][N] and uint8 [N/32][M].
+ * Experts with no rows cost nothing.
+ */
+moe_status moe_grouped_fp8_gemm_fwd(const void* a, const float* a_scales, int64_t M,
+                                    const moe_fp8_weight* w, const moe_groups* g, int32_t epi,
+                                    void* out, float* out_scales, void* saved, void* saved_scales,
+                                    void* stream);
+
+/*
+ * moe_grouped_fp8_gemm_bwd_dx -- activation gradient through the same weights,
+ * read in place: acc[p][k] = sum_b d_scales[b][p] * w.scales[e][b][k/128] *
+ * sum_{n in block b} dout[p][n] * w.q[e][n][k].
+ *  dout, d_scales  FP8 rows [M][N] of the upstream gradient.
+ *  epi   MOE_EPI_NONE: din bf16 [M][K]; din_scales, saved, saved_scales NULL.
+ *        MOE_EPI_SWIGLU_BWD (down projection, K % 128 == 0): acc = dh; with g
+ *        and u from the 8-bit checkpoint (e4m3 [M][2K], uint8 [2K/32][M]),
+ *        s = sigmoid(g): din, din_scales = FP8 rows [M][2K] of
+ *        bf16([dh*u*s*(1+g*(1-s)) | dh*g*s]), the dout of the gate/up product.
+ */
+moe_status moe_grouped_fp8_gemm_bwd_dx(const void* dout, const float* d_scales, int64_t M,
+                                       const moe_fp8_weight* w, const moe_groups* g, int32_t epi,
+                                       const void* saved, const void* saved_scales, void* din,
+                                       float* din_scales, void* stream);
+
 /* Synchronizes `stream`, then reads and clears the device error word of the
  * current device (MOE_DEVERR_*). Debug/test use. */
 moe_status moe_get_device_error(int32_t* code, void* stream);

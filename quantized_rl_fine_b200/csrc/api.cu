@@ -4,11 +4,13 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
 #include "common.cuh"
 #include "dequant.cuh"
+#include "fp8_gemm.cuh"
 #include "gemm.cuh"
 #include "launchers.cuh"
 
@@ -359,6 +361,34 @@ GemmPlan plan_gemm(int mode, int64_t M, const moe_qweight* w, int F, int tile_f,
   return pl;
 }
 
+moe_status check_router(const moe_router* r, int E, int k) {
+  if (!r) return MOE_ERR_INVALID_ARG;
+  if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if (r->groups < 1 || r->groups > 32 || E % r->groups != 0) return MOE_ERR_INVALID_ARG;
+  if (r->topk_groups < 1 || r->topk_groups > r->groups) return MOE_ERR_INVALID_ARG;
+  if (r->group_top != 1 && r->group_top != 2) return MOE_ERR_INVALID_ARG;
+  if (k > r->topk_groups * (E / r->groups)) return MOE_ERR_INVALID_ARG;
+  if ((r->renorm != 0 && r->renorm != 1) || !std::isfinite(r->scale)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+moe_status check_fp8_weight(const moe_fp8_weight* w) {
+  if (!w || !w->q || !w->scales) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(w->q) || !aligned16(w->scales)) return MOE_ERR_MISALIGNED;
+  if (w->E < 1 || w->E > 1024 || w->N < 1 || w->K < 1) return MOE_ERR_INVALID_ARG;
+  if (w->K % 16 != 0 || w->N % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  // a tensor-map stride is below 2^40 bytes
+  if (static_cast<int64_t>(w->N) * w->K >= (int64_t(1) << 40)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// [a, a + na) and [b, b + nb) share a byte.
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const char* x = static_cast<const char*>(a);
+  const char* y = static_cast<const char*>(b);
+  return x < y + nb && y < x + na;
+}
+
 moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 // Workspace convention: ws == NULL with ws_bytes != NULL is a size query
@@ -477,6 +507,60 @@ moe_status run_gemm(int mode, int epi, const void* bmat, int64_t M, const moe_qw
   p.saved = static_cast<__nv_bfloat16*>(saved);
   return cuda_status(launch_grouped_qgemm(mode, w->fmt, epi, pl.lanes, pl.dq_warps, pl.pair, tb, tw,
                                           ts, p, pl.grid, pl.smem, s));
+}
+
+// One FP8 grouped product (forward or backward) over the rows `rows` [M][R].
+moe_status run_fp8_gemm(bool bwd, int epi, const void* rows, const float* row_scales, int64_t M,
+                        const moe_fp8_weight* w, const moe_groups* g, void* out, float* out_scales,
+                        void* saved, void* saved_scales, cudaStream_t s) {
+  const int R = bwd ? w->N : w->K;
+  const int F = bwd ? w->K : (epi == MOE_EPI_SWIGLU ? w->N / 2 : w->N);
+  const int tile_f = (!bwd && epi == MOE_EPI_SWIGLU) ? 128 : 256;
+  CUtensorMap ta, tw;
+  // Rows and weights as boxes of 128 bytes x 128 rows, 128-byte swizzle; what
+  // lies past the reduction length, the features or the rows reads as zeros.
+  const uint64_t N = w->N, K = w->K, E = w->E, rl = R;
+  const uint64_t ad[3] = {rl, static_cast<uint64_t>(M), 1};
+  const uint64_t as[2] = {rl, rl * static_cast<uint64_t>(M)};
+  const uint64_t wd[3] = {K, N, E};
+  const uint64_t wst[2] = {K, N * K};
+  const uint32_t box[3] = {128, 128, 1};
+  if (!make_map_3d(&ta, rows, CU_TENSOR_MAP_DATA_TYPE_UINT8, ad, as, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map_3d(&tw, w->q, CU_TENSOR_MAP_DATA_TYPE_UINT8, wd, wst, box, CU_TENSOR_MAP_SWIZZLE_128B))
+    return MOE_ERR_CUDA;
+  Fp8GemmArgs p;
+  p.offsets = g->expert_offsets;
+  p.active = g->active;
+  p.num_active = g->num_active;
+  p.E = w->E;
+  p.N = w->N;
+  p.K = w->K;
+  p.M = static_cast<int32_t>(M);
+  p.R = R;
+  p.n_ftiles = (F + tile_f - 1) / tile_f;
+  p.a_scales = row_scales;
+  p.w_scales = w->scales;
+  p.out = static_cast<uint8_t*>(out);
+  p.out_scales = out_scales;
+  p.saved = static_cast<uint8_t*>(saved);
+  p.saved_scales = static_cast<uint8_t*>(saved_scales);
+  // the most tiles that M rows over E experts can make; the list is 32-bit
+  const int64_t bound = static_cast<int64_t>(p.n_ftiles) * (std::min<int64_t>(w->E, M) + M / 128 + 1);
+  if (bound >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  const int grid = static_cast<int>(std::min<int64_t>(num_sms(), bound));
+  return cuda_status(launch_grouped_fp8_gemm(bwd, epi, ta, tw, p, grid, s));
+}
+
+// Checks shared by the two FP8 products.
+moe_status check_fp8_call(const void* rows, const float* row_scales, int64_t M, const moe_fp8_weight* w,
+                          const moe_groups* g, const void* out) {
+  moe_status st = check_fp8_weight(w);
+  if (st != MOE_OK) return st;
+  if (M < 1 || M >= (int64_t(1) << 31)) return MOE_ERR_INVALID_ARG;
+  if ((st = check_groups(g, w->E)) != MOE_OK) return st;
+  if (!rows || !row_scales || !out) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(rows) || !aligned16(row_scales) || !aligned16(out)) return MOE_ERR_MISALIGNED;
+  return MOE_OK;
 }
 
 }  // namespace
@@ -735,6 +819,141 @@ moe_status moe_unpermute_combine(const void* rows, const int32_t* inv_perm, cons
     return MOE_ERR_MISALIGNED;
   return cuda_status(launch_combine(rows, inv_perm, gates, static_cast<int>(T), k, D, out, mode,
                                     static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_route_scored(const float* logits, const float* bias, const void* x, int64_t T,
+                            int32_t E, int32_t k, int64_t d, const moe_router* router,
+                            int32_t chunk_size, int32_t* topk_idx, float* gates,
+                            int32_t* expert_offsets, int32_t* active, int32_t* num_active,
+                            int32_t* chunk_offsets, int32_t* num_chunks, int32_t* perm_token,
+                            int32_t* inv_perm, void* x_perm, void* ws, size_t* ws_bytes,
+                            void* stream) {
+  MOEQ_TRACE("moe_route_scored");
+  if (T < 1 || E < 1 || E > 1024 || k < 1 || k > 32 || k > E || chunk_size < 1)
+    return MOE_ERR_INVALID_ARG;
+  if (T >= (int64_t(1) << 31) || T * k >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  moe_status st = check_router(router, E, k);
+  if (st != MOE_OK) return st;
+  const size_t need = route_single_pass(T, E)
+                          ? 0
+                          : align_up(static_cast<size_t>(route_num_blocks(T)) * E * sizeof(int32_t), 256);
+  if ((st = check_workspace(ws, ws_bytes, need)) != MOE_OK) return st;
+  if (!ws && ws_bytes) return MOE_OK;   // size query
+  const void* ptrs[] = {logits, topk_idx, gates, expert_offsets, active, num_active,
+                        chunk_offsets, num_chunks, perm_token, inv_perm};
+  for (const void* p : ptrs) {
+    if (!p) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(p)) return MOE_ERR_MISALIGNED;
+  }
+  if (bias && !aligned16(bias)) return MOE_ERR_MISALIGNED;
+  if (x) {
+    if (!x_perm || d < 8 || d % 8 != 0) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(x_perm)) return MOE_ERR_MISALIGNED;
+  }
+  return cuda_status(launch_route_scored(logits, bias, x, static_cast<int>(T), E, k, d, *router,
+                                         chunk_size, topk_idx, gates, expert_offsets, active,
+                                         num_active, chunk_offsets, num_chunks, perm_token, inv_perm,
+                                         x ? x_perm : nullptr, static_cast<int32_t*>(ws),
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_route_scored_bwd(const float* d_gates, const float* logits, const int32_t* topk_idx,
+                                int64_t T, int32_t E, int32_t k, const moe_router* router,
+                                float* d_logits, void* stream) {
+  MOEQ_TRACE("moe_route_scored_bwd");
+  if (T < 1 || E < 1 || E > 1024 || k < 1 || k > 32 || k > E) return MOE_ERR_INVALID_ARG;
+  if (T >= (int64_t(1) << 31) || T * k >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (!router || (router->score != MOE_SCORE_SOFTMAX && router->score != MOE_SCORE_SIGMOID) ||
+      (router->renorm != 0 && router->renorm != 1) || !std::isfinite(router->scale))
+    return MOE_ERR_INVALID_ARG;
+  if (!d_gates || !logits || !topk_idx || !d_logits) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(d_gates) || !aligned16(logits) || !aligned16(topk_idx) || !aligned16(d_logits))
+    return MOE_ERR_MISALIGNED;
+  return cuda_status(launch_route_scored_bwd(d_gates, logits, topk_idx, static_cast<int>(T), E, k,
+                                             *router, d_logits, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_combine_bwd(const void* dy, const void* rows, const int32_t* inv_perm,
+                           const float* gates, int64_t T, int32_t k, int64_t D, void* d_rows,
+                           float* d_gates, void* stream) {
+  MOEQ_TRACE("moe_combine_bwd");
+  if (!dy || !rows || !inv_perm || !d_rows || !d_gates) return MOE_ERR_INVALID_ARG;
+  if (T < 1 || k < 1 || k > 32 || D < 8 || D % 8 != 0) return MOE_ERR_INVALID_ARG;
+  if (T >= (int64_t(1) << 31) || T * k >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (!aligned16(dy) || !aligned16(rows) || !aligned16(inv_perm) || !aligned16(d_rows) ||
+      !aligned16(d_gates) || (gates && !aligned16(gates)))
+    return MOE_ERR_MISALIGNED;
+  const int64_t nb = T * D * 2;
+  if (overlap(d_rows, nb * k, rows, nb * k) || overlap(d_rows, nb * k, dy, nb))
+    return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_combine_bwd(dy, rows, inv_perm, gates, static_cast<int>(T), k, D, d_rows,
+                                        d_gates, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_quantize_fp8_rows(const void* x, int64_t T, int64_t K, const int32_t* inv_perm,
+                                 int32_t k, void* q, float* scales, void* stream) {
+  MOEQ_TRACE("moe_quantize_fp8_rows");
+  if (!x || !q || !scales || T < 1 || K < 1 || k < 1 || k > 32) return MOE_ERR_INVALID_ARG;
+  if (!inv_perm && k != 1) return MOE_ERR_INVALID_ARG;
+  if (K % 16 != 0 || K >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (T >= (int64_t(1) << 31) || T * k >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (!aligned16(x) || !aligned16(q) || !aligned16(scales) || (inv_perm && !aligned16(inv_perm)))
+    return MOE_ERR_MISALIGNED;
+  return cuda_status(launch_quantize_fp8_rows(x, static_cast<int>(T), K, inv_perm, k, q, scales,
+                                              static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_dequantize_fp8_rows(const void* q, const void* scales, int64_t M, int64_t K,
+                                   int32_t fmt, void* out, void* stream) {
+  MOEQ_TRACE("moe_dequantize_fp8_rows");
+  if (!q || !scales || !out || M < 1 || K < 1) return MOE_ERR_INVALID_ARG;
+  if (fmt != MOE_FP8_BLOCK128_F32 && fmt != MOE_FP8_BLOCK32_E8M0) return MOE_ERR_INVALID_ARG;
+  if (K % 16 != 0 || K >= (int64_t(1) << 31) || M >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(scales) || !aligned16(out)) return MOE_ERR_MISALIGNED;
+  return cuda_status(launch_dequantize_fp8_rows(q, scales, static_cast<int>(M), K, fmt, out,
+                                                static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_grouped_fp8_gemm_fwd(const void* a, const float* a_scales, int64_t M,
+                                    const moe_fp8_weight* w, const moe_groups* g, int32_t epi,
+                                    void* out, float* out_scales, void* saved, void* saved_scales,
+                                    void* stream) {
+  MOEQ_TRACE("moe_grouped_fp8_gemm_fwd");
+  moe_status st = check_fp8_call(a, a_scales, M, w, g, out);
+  if (st != MOE_OK) return st;
+  if (epi == MOE_EPI_NONE) {
+    if (out_scales || saved || saved_scales) return MOE_ERR_INVALID_ARG;
+  } else if (epi == MOE_EPI_SWIGLU) {
+    if (w->N % 256 != 0) return MOE_ERR_UNSUPPORTED;
+    if (!out_scales || !saved != !saved_scales) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(out_scales) || (saved && (!aligned16(saved) || !aligned16(saved_scales))))
+      return MOE_ERR_MISALIGNED;
+  } else {
+    return MOE_ERR_INVALID_ARG;
+  }
+  return run_fp8_gemm(false, epi, a, a_scales, M, w, g, out, out_scales, saved, saved_scales,
+                      static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_grouped_fp8_gemm_bwd_dx(const void* dout, const float* d_scales, int64_t M,
+                                       const moe_fp8_weight* w, const moe_groups* g, int32_t epi,
+                                       const void* saved, const void* saved_scales, void* din,
+                                       float* din_scales, void* stream) {
+  MOEQ_TRACE("moe_grouped_fp8_gemm_bwd_dx");
+  moe_status st = check_fp8_call(dout, d_scales, M, w, g, din);
+  if (st != MOE_OK) return st;
+  if (epi == MOE_EPI_NONE) {
+    if (din_scales || saved || saved_scales) return MOE_ERR_INVALID_ARG;
+  } else if (epi == MOE_EPI_SWIGLU_BWD) {
+    if (w->K % 128 != 0) return MOE_ERR_UNSUPPORTED;
+    if (!din_scales || !saved || !saved_scales) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(din_scales) || !aligned16(saved) || !aligned16(saved_scales))
+      return MOE_ERR_MISALIGNED;
+  } else {
+    return MOE_ERR_INVALID_ARG;
+  }
+  return run_fp8_gemm(true, epi, dout, d_scales, M, w, g, din, din_scales, const_cast<void*>(saved),
+                      const_cast<void*>(saved_scales), static_cast<cudaStream_t>(stream));
 }
 
 moe_status moe_get_device_error(int32_t* code, void* stream) {

@@ -4,6 +4,8 @@
 //
 // One warp per token; each lane moves 16-byte slices (8 BF16) of the rows,
 // so every row access is a fully coalesced 512-byte warp transaction.
+#include <algorithm>
+
 #include "launchers.cuh"
 #include "common.cuh"
 
@@ -94,7 +96,85 @@ __global__ void scatter_kernel(const uint4* __restrict__ rows, const int32_t* __
   }
 }
 
+// One block per token, 16-byte slices of the row over its threads: dy is read
+// once, each of the token's k rows once, and gate * dy written once to each of
+// the k slots (bf16_of_product: one rounding, the bits of scatter_kernel). The
+// k dot products accumulate in FP32 per thread in ascending slice order, then
+// over lanes and warps in a fixed order.
+template <int KMAX>
+__global__ void __launch_bounds__(256)
+combine_bwd_kernel(const uint4* __restrict__ dy, const uint4* __restrict__ rows,
+                   const int32_t* __restrict__ inv_perm, const float* __restrict__ gates, int k,
+                   int64_t dvec, uint4* __restrict__ d_rows, float* __restrict__ d_gates) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  __shared__ float part[8][KMAX];
+  const int64_t t = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = blockDim.x >> 5;
+  int64_t base[KMAX];
+  float g[KMAX], acc[KMAX];
+#pragma unroll
+  for (int j = 0; j < KMAX; ++j) {
+    base[j] = (j < k) ? static_cast<int64_t>(__ldg(inv_perm + t * k + j)) * dvec : 0;
+    g[j] = (j < k && gates) ? __ldg(gates + t * k + j) : 1.0f;
+    acc[j] = 0.0f;
+  }
+  for (int64_t c = threadIdx.x; c < dvec; c += blockDim.x) {
+    uint4 r[KMAX];
+    const uint4 dv = __ldg(dy + t * dvec + c);
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j)
+      if (j < k) r[j] = __ldg(rows + base[j] + c);
+    float f[8];
+    unpack8(dv, f);
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j) {
+      if (j >= k) continue;
+      float y[8];
+      unpack8(r[j], y);
+      uint32_t h[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        acc[j] = fmaf(f[i], y[i], acc[j]);
+        h[i] = bf16_of_product(g[j], f[i]);
+      }
+      d_rows[base[j] + c] = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16),
+                                       h[6] | (h[7] << 16));
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < KMAX; ++j) {
+    if (j >= k) continue;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
+    if (lane == 0) part[warp][j] = acc[j];
+  }
+  __syncthreads();
+  for (int j = threadIdx.x; j < k; j += blockDim.x) {
+    float s = 0.0f;
+    for (int w = 0; w < nwarps; ++w) s += part[w][j];
+    d_gates[t * k + j] = s;
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_combine_bwd(const void* dy, const void* rows, const int32_t* inv_perm,
+                               const float* gates, int T, int k, int64_t D, void* d_rows,
+                               float* d_gates, cudaStream_t s) {
+  const int64_t dvec = D / 8;
+  const int threads = static_cast<int>(std::min<int64_t>(256, (dvec + 31) / 32 * 32));
+#define MOEQ_CB(K_)                                                                                 \
+  launch_pdl(combine_bwd_kernel<K_>, dim3(T), dim3(threads), 0, s, static_cast<const uint4*>(dy),   \
+             static_cast<const uint4*>(rows), inv_perm, gates, k, dvec, static_cast<uint4*>(d_rows), \
+             d_gates)
+  if (k <= 2) return MOEQ_CB(2);
+  if (k <= 4) return MOEQ_CB(4);
+  if (k <= 8) return MOEQ_CB(8);
+  if (k <= 16) return MOEQ_CB(16);
+  return MOEQ_CB(32);
+#undef MOEQ_CB
+}
 
 cudaError_t launch_combine(const void* rows, const int32_t* inv_perm, const float* gates, int T,
                            int k, int64_t D, void* out, int mode, cudaStream_t s) {

@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/moeq.h"
+
 namespace moeq {
 
 int route_num_blocks(int64_t T);
@@ -18,6 +20,32 @@ cudaError_t launch_route(const float* logits, const void* x, int T, int E, int k
                          int32_t* active, int32_t* num_active, int32_t* chunk_offsets,
                          int32_t* num_chunks, int32_t* perm_token, int32_t* inv_perm,
                          void* x_perm, int32_t* block_counts, cudaStream_t s);
+// The part after the selection: group tables, permutation, permuted rows.
+cudaError_t launch_route_tables(const void* x, int T, int E, int k, int64_t d, int chunk_size,
+                                const int32_t* topk_idx, int32_t* offsets, int32_t* active,
+                                int32_t* num_active, int32_t* chunk_offsets, int32_t* num_chunks,
+                                int32_t* perm_token, int32_t* inv_perm, void* x_perm,
+                                int32_t* block_counts, cudaStream_t s);
+int route_tokens_per_block();
+// Scored routing; block_counts as in launch_route.
+cudaError_t launch_route_scored(const float* logits, const float* bias, const void* x, int T, int E,
+                                int k, int64_t d, const moe_router& rt, int chunk_size,
+                                int32_t* topk_idx, float* gates, int32_t* offsets, int32_t* active,
+                                int32_t* num_active, int32_t* chunk_offsets, int32_t* num_chunks,
+                                int32_t* perm_token, int32_t* inv_perm, void* x_perm,
+                                int32_t* block_counts, cudaStream_t s);
+cudaError_t launch_route_scored_bwd(const float* d_gates, const float* logits,
+                                    const int32_t* topk_idx, int T, int E, int k,
+                                    const moe_router& rt, float* d_logits, cudaStream_t s);
+// d_rows = gate * dy scattered to the slots, d_gates = dy . rows, in one pass.
+cudaError_t launch_combine_bwd(const void* dy, const void* rows, const int32_t* inv_perm,
+                               const float* gates, int T, int k, int64_t D, void* d_rows,
+                               float* d_gates, cudaStream_t s);
+// BF16 rows -> e4m3 rows with power-of-two scales per 1 x 128 block, written to k rows each.
+cudaError_t launch_quantize_fp8_rows(const void* x, int T, int64_t K, const int32_t* inv_perm, int k,
+                                     void* q, float* scales, cudaStream_t s);
+cudaError_t launch_dequantize_fp8_rows(const void* q, const void* scales, int M, int64_t K, int fmt,
+                                       void* out, cudaStream_t s);
 cudaError_t launch_combine(const void* rows, const int32_t* inv_perm, const float* gates, int T,
                            int k, int64_t D, void* out, int mode, cudaStream_t s);
 // out = x . R_e for the rows of each expert (forward adapter); with rows (not

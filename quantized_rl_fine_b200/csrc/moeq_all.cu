@@ -5,5 +5,8 @@
 #include "adapter.cu"
 #include "combine.cu"
 #include "ep.cu"
+#include "fp8.cu"
 #include "gemm.cu"
+#include "fp8_gemm.cu"
 #include "route.cu"
+#include "router.cu"

@@ -409,7 +409,6 @@ cudaError_t launch_route(const float* logits, const void* x, int T, int E, int k
                          int32_t* active, int32_t* num_active, int32_t* chunk_offsets,
                          int32_t* num_chunks, int32_t* perm_token, int32_t* inv_perm,
                          void* x_perm, int32_t* block_counts, cudaStream_t s) {
-  const int W = (T + 31) / 32;
   // Small launches: one token per warp, then the single-block tail.
   const bool small = route_single_pass(T, E);
   if (!small && block_counts == nullptr) return cudaErrorInvalidValue;
@@ -431,6 +430,24 @@ cudaError_t launch_route(const float* logits, const void* x, int T, int E, int k
   else err = MOEQ_TOPK(32);
 #undef MOEQ_TOPK
   if (err != cudaSuccess) return err;
+  return launch_route_tables(x, T, E, k, d, chunk_size, topk_idx, offsets, active, num_active,
+                             chunk_offsets, num_chunks, perm_token, inv_perm, x_perm, block_counts,
+                             s);
+}
+
+int route_tokens_per_block() { return kRouteTokensPerBlock; }
+
+// From the selection (and, past the single-pass sizes, its per-block
+// histograms) to the group tables, the permutation and the permuted rows.
+cudaError_t launch_route_tables(const void* x, int T, int E, int k, int64_t d, int chunk_size,
+                                const int32_t* topk_idx, int32_t* offsets, int32_t* active,
+                                int32_t* num_active, int32_t* chunk_offsets, int32_t* num_chunks,
+                                int32_t* perm_token, int32_t* inv_perm, void* x_perm,
+                                int32_t* block_counts, cudaStream_t s) {
+  const int W = (T + 31) / 32;
+  const bool small = route_single_pass(T, E);
+  const int nblk = route_num_blocks(T);
+  cudaError_t err;
   if (small) {
     int sm_count = 0;
     err = route_prepare_device(&sm_count);
@@ -447,8 +464,7 @@ cudaError_t launch_route(const float* logits, const void* x, int T, int E, int k
       blocks = (M + kTailRowsPerBlock - 1) / kTailRowsPerBlock;
     }
     return launch_pdl(route_tail_kernel, dim3(blocks), dim3(1024), tsm, s,
-                      static_cast<const int32_t*>(topk_idx), T, E, k, chunk_size, offsets,
-                      active, num_active, chunk_offsets, num_chunks, perm_token, inv_perm,
+                      topk_idx, T, E, k, chunk_size, offsets, active, num_active, chunk_offsets, num_chunks, perm_token, inv_perm,
                       static_cast<const uint4*>(x), static_cast<uint4*>(x_perm), d / 8);
   } else {
     err = launch_pdl(route_scan_kernel, dim3(1), dim3(1024), 0, s, block_counts, nblk, E,
@@ -456,7 +472,7 @@ cudaError_t launch_route(const float* logits, const void* x, int T, int E, int k
     if (err != cudaSuccess) return err;
     const size_t sm = 2 * E * sizeof(uint32_t);
     err = launch_pdl(route_scatter_kernel, dim3(nblk), dim3(kRouteThreads), sm, s,
-                     static_cast<const int32_t*>(topk_idx), static_cast<const int32_t*>(block_counts),
+                     topk_idx, static_cast<const int32_t*>(block_counts),
                      static_cast<const int32_t*>(offsets), T, E, k, perm_token, inv_perm);
   }
   if (err != cudaSuccess || x == nullptr) return err;

@@ -8,6 +8,7 @@ device is present, every call raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -32,7 +33,11 @@ DEVERR_NONE, DEVERR_WAIT_TIMEOUT, DEVERR_BAD_OFFSETS = 0, 1, 2
 EXPORTED = ("moe_route_permute", "moe_route_permute_noalloc", "moe_grouped_qgemm_fwd", "moe_grouped_qgemm_bwd_dx",
             "moe_unpermute_combine", "moe_get_device_error", "moe_status_string",
             "moe_abi_version", "moe_test_dequant", "moe_test_set_wait_budget",
-            "moe_dequant_experts", "moe_ep_regroup", "moe_nvtx_enabled")
+            "moe_dequant_experts", "moe_ep_regroup", "moe_nvtx_enabled", "moe_route_scored",
+            "moe_route_scored_bwd", "moe_combine_bwd", "moe_quantize_fp8_rows",
+            "moe_dequantize_fp8_rows", "moe_grouped_fp8_gemm_fwd", "moe_grouped_fp8_gemm_bwd_dx")
+SCORE = {"softmax": 1, "sigmoid": 2}
+FP8_BLOCK128_F32, FP8_BLOCK32_E8M0 = 1, 2
 
 
 class MoeError(RuntimeError):
@@ -51,6 +56,16 @@ class GroupsC(ctypes.Structure):
     _fields_ = [("expert_offsets", ctypes.c_void_p), ("active", ctypes.c_void_p),
                 ("num_active", ctypes.c_void_p), ("chunk_offsets", ctypes.c_void_p),
                 ("num_chunks", ctypes.c_void_p), ("E", ctypes.c_int32)]
+
+
+class RouterC(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class Fp8WeightC(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("E", ctypes.c_int32),
+                ("N", ctypes.c_int32), ("K", ctypes.c_int32)]
 
 
 _lib = None
@@ -84,6 +99,16 @@ def lib() -> ctypes.CDLL:
     L.moe_test_set_wait_budget.argtypes = [i64]
     L.moe_dequant_experts.argtypes = [ctypes.POINTER(QWeightC), vp, i32, vp, vp]
     L.moe_ep_regroup.argtypes = [vp, i32, i32, i64, vp, vp, i64, i32, i32, vp, vp, vp, vp, vp, vp]
+    rp, fp = ctypes.POINTER(RouterC), ctypes.POINTER(Fp8WeightC)
+    gp = ctypes.POINTER(GroupsC)
+    L.moe_route_scored.argtypes = [vp, vp, vp, i64, i32, i32, i64, rp, i32, vp, vp, vp, vp, vp, vp, vp,
+                                   vp, vp, vp, vp, sz, vp]
+    L.moe_route_scored_bwd.argtypes = [vp, vp, vp, i64, i32, i32, rp, vp, vp]
+    L.moe_combine_bwd.argtypes = [vp, vp, vp, vp, i64, i32, i64, vp, vp, vp]
+    L.moe_quantize_fp8_rows.argtypes = [vp, i64, i64, vp, i32, vp, vp, vp]
+    L.moe_dequantize_fp8_rows.argtypes = [vp, vp, i64, i64, i32, vp, vp]
+    L.moe_grouped_fp8_gemm_fwd.argtypes = [vp, vp, i64, fp, gp, i32, vp, vp, vp, vp, vp]
+    L.moe_grouped_fp8_gemm_bwd_dx.argtypes = [vp, vp, i64, fp, gp, i32, vp, vp, vp, vp, vp]
     for name in EXPORTED:
         if name not in ("moe_status_string",):
             getattr(L, name).restype = ctypes.c_int32
@@ -309,6 +334,332 @@ def moe_ep_regroup(counts: torch.Tensor, rows: torch.Tensor, direction: int, chu
     groups = Routing(topk_idx=None, gates=None, perm_token=None, inv_perm=None, x_perm=out,
                      E=E_loc, k=1, **t)
     return out, groups
+
+
+# --------------------------------------------------------------------------
+# Scored routing, router gradient, FP8 rows and FP8 expert products
+#
+# These calls check dtype, shape, layout (contiguous) and device of every
+# tensor, run on the tensors' own device, and allocate their outputs and
+# workspaces on the stream they launch on.
+# --------------------------------------------------------------------------
+
+def _need(t, name: str, dtype, shape, device=None):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: libmoeq takes CUDA tensors only")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+
+
+@contextlib.contextmanager
+def _switch(device, stream):
+    with torch.cuda.device(device):
+        with torch.cuda.stream(stream):       # None: the device's current stream
+            yield
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device, stream):
+    """The tensors' device, and `stream` (if any) as its current stream."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return _HERE
+    return _switch(device, stream)
+
+
+@dataclass(frozen=True)
+class RouterSpec:
+    """How moe_route_scored selects experts and forms gates (moe_router in moeq.h)."""
+    score: str = "softmax"        # "softmax" (over all experts) or "sigmoid"
+    groups: int = 1               # expert groups of E / groups consecutive experts
+    topk_groups: int = 1          # groups a token may choose from
+    group_top: int = 1            # a group's score: sum of its 1 or 2 largest keys
+    renorm: bool = True           # gates divided by the sum of the selected scores
+    scale: float = 1.0            # factor of every gate
+
+    def c(self) -> RouterC:
+        if self.score not in SCORE:
+            raise ValueError(f"score {self.score!r}: expected one of {sorted(SCORE)}")
+        return RouterC(SCORE[self.score], self.groups, self.topk_groups, self.group_top,
+                       1 if self.renorm else 0, self.scale)
+
+
+def _new_routing(T: int, E: int, k: int, d: int | None, dev) -> Routing:
+    # one allocation for the eight int32 tables, each starting on 16 bytes
+    sizes = (T * k, E + 1, E, 1, E + 1, 1, T * k, T * k)
+    flat = torch.empty(sum(-(-n // 4) * 4 for n in sizes), dtype=torch.int32, device=dev)
+    parts, at = [], 0
+    for n in sizes:
+        parts.append(flat[at:at + n])
+        at += -(-n // 4) * 4
+    return Routing(topk_idx=parts[0].view(T, k),
+                   gates=torch.empty((T, k), dtype=torch.float32, device=dev),
+                   expert_offsets=parts[1], active=parts[2], num_active=parts[3],
+                   chunk_offsets=parts[4], num_chunks=parts[5], perm_token=parts[6],
+                   inv_perm=parts[7],
+                   x_perm=None if d is None else torch.empty((T * k, d), dtype=torch.bfloat16, device=dev),
+                   E=E, k=k)
+
+
+def _need_routing(r: Routing, T: int, E: int, k: int, d: int | None, dev):
+    i32 = torch.int32
+    for name, n in (("expert_offsets", E + 1), ("active", E), ("num_active", 1),
+                    ("chunk_offsets", E + 1), ("num_chunks", 1), ("perm_token", T * k),
+                    ("inv_perm", T * k)):
+        _need(getattr(r, name), "out." + name, i32, (n,), dev)
+    _need(r.topk_idx, "out.topk_idx", i32, (T, k), dev)
+    _need(r.gates, "out.gates", torch.float32, (T, k), dev)
+    if d is not None:
+        _need(r.x_perm, "out.x_perm", torch.bfloat16, (T * k, d), dev)
+
+
+def moe_route_scored(logits: torch.Tensor, x: torch.Tensor | None, k: int, chunk_size: int,
+                     router: RouterSpec, bias: torch.Tensor | None = None, stream=None,
+                     out: Routing | None = None) -> Routing:
+    """moe_route_permute with softmax or sigmoid scores, a selection bias [E], expert groups and
+    renormalised or plain gates."""
+    if logits.dim() != 2:
+        raise ValueError("logits: expected [T, E]")
+    T, E = logits.shape
+    dev = logits.device
+    _need(logits, "logits", torch.float32, (T, E))
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (E,), dev)
+    d = None
+    if x is not None:
+        d = x.shape[-1]
+        _need(x, "x", torch.bfloat16, (T, d), dev)
+    rc = router.c()
+    with _on(dev, stream):
+        L = lib()
+        st = _stream()
+        wsb = ctypes.c_size_t(0)
+        _check(L.moe_route_scored(None, None, None, T, E, k, d or 0, ctypes.byref(rc), chunk_size, None,
+                                  None, None, None, None, None, None, None, None, None, None,
+                                  ctypes.byref(wsb), st), "moe_route_scored (workspace query)")
+        if out is None:
+            out = _new_routing(T, E, k, d, dev)
+        else:
+            _need_routing(out, T, E, k, d, dev)
+        ws, wsp, wsz = _workspace(wsb.value, dev)
+        _check(L.moe_route_scored(_p(logits), _p(bias), _p(x), T, E, k, d or 0, ctypes.byref(rc),
+                                  chunk_size, _p(out.topk_idx), _p(out.gates), _p(out.expert_offsets),
+                                  _p(out.active), _p(out.num_active), _p(out.chunk_offsets),
+                                  _p(out.num_chunks), _p(out.perm_token), _p(out.inv_perm),
+                                  _p(out.x_perm) if x is not None else None, wsp, wsz, st),
+               "moe_route_scored")
+    return out
+
+
+def moe_route_scored_bwd(d_gates: torch.Tensor, logits: torch.Tensor, routing: Routing,
+                         router: RouterSpec, stream=None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """d_logits [T, E] from the gates' gradient [T, k] and the selection in `routing`."""
+    if logits.dim() != 2:
+        raise ValueError("logits: expected [T, E]")
+    T, E = logits.shape
+    k, dev = routing.k, logits.device
+    _need(logits, "logits", torch.float32, (T, E))
+    _need(d_gates, "d_gates", torch.float32, (T, k), dev)
+    _need(routing.topk_idx, "routing.topk_idx", torch.int32, (T, k), dev)
+    rc = router.c()
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((T, E), dtype=torch.float32, device=dev)
+        else:
+            _need(out, "out", torch.float32, (T, E), dev)
+        _check(lib().moe_route_scored_bwd(_p(d_gates), _p(logits), _p(routing.topk_idx), T, E, k,
+                                          ctypes.byref(rc), _p(out), _stream()), "moe_route_scored_bwd")
+    return out
+
+
+def moe_combine_bwd(dy: torch.Tensor, rows: torch.Tensor, routing: Routing, stream=None,
+                    out: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Backward of the combine: (d_rows [T*k, D] = gate * dy per slot, d_gates [T, k] = dy . rows)."""
+    if dy.dim() != 2:
+        raise ValueError("dy: expected [T, D]")
+    T, D = dy.shape
+    k, dev = routing.k, dy.device
+    _need(dy, "dy", torch.bfloat16, (T, D))
+    _need(rows, "rows", torch.bfloat16, (T * k, D), dev)
+    _need(routing.inv_perm, "routing.inv_perm", torch.int32, (T * k,), dev)
+    if routing.gates is not None:
+        _need(routing.gates, "routing.gates", torch.float32, (T, k), dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((T * k, D), dtype=torch.bfloat16, device=dev)
+        else:
+            _need(out, "out", torch.bfloat16, (T * k, D), dev)
+        d_gates = torch.empty((T, k), dtype=torch.float32, device=dev)
+        _check(lib().moe_combine_bwd(_p(dy), _p(rows), _p(routing.inv_perm), _p(routing.gates), T, k, D,
+                                     _p(out), _p(d_gates), _stream()), "moe_combine_bwd")
+    return out, d_gates
+
+
+@dataclass
+class Fp8Rows:
+    """e4m3 rows and their block scales: fp32 [ceil(K/128), M] (FP8 rows) or uint8 E8M0
+    [K/32, M] (8-bit checkpoint of saved activations)."""
+    q: torch.Tensor               # [M, K] float8_e4m3fn
+    scales: torch.Tensor
+
+    @property
+    def fmt(self) -> int:
+        return FP8_BLOCK32_E8M0 if self.scales.dtype == torch.uint8 else FP8_BLOCK128_F32
+
+    def nbytes(self) -> int:
+        return self.q.numel() + self.scales.numel() * self.scales.element_size()
+
+
+@dataclass
+class Fp8WeightT:
+    """FP8 expert stack: e4m3 [E, N, K] and one fp32 scale per 128 x 128 block."""
+    q: torch.Tensor               # [E, N, K] float8_e4m3fn
+    scales: torch.Tensor          # [E, ceil(N/128), ceil(K/128)] float32
+
+    @property
+    def E(self):
+        return self.q.shape[0]
+
+    @property
+    def N(self):
+        return self.q.shape[1]
+
+    @property
+    def K(self):
+        return self.q.shape[2]
+
+    def to(self, device) -> "Fp8WeightT":
+        return Fp8WeightT(self.q.to(device), self.scales.to(device))
+
+    def nbytes(self) -> int:
+        return self.q.numel() + 4 * self.scales.numel()
+
+
+def _need_fp8_rows(r: Fp8Rows, name: str, M: int, K: int, device, e8m0: bool = False):
+    _need(r.q, name + ".q", torch.float8_e4m3fn, (M, K), device)
+    if e8m0:
+        _need(r.scales, name + ".scales", torch.uint8, (-(-K // 32), M), device)
+    else:
+        _need(r.scales, name + ".scales", torch.float32, (-(-K // 128), M), device)
+
+
+def _new_fp8_rows(M: int, K: int, device, e8m0: bool = False) -> Fp8Rows:
+    scales = (torch.empty((-(-K // 32), M), dtype=torch.uint8, device=device) if e8m0 else
+              torch.empty((-(-K // 128), M), dtype=torch.float32, device=device))
+    return Fp8Rows(torch.empty((M, K), dtype=torch.float8_e4m3fn, device=device), scales)
+
+
+def _fp8_weight_c(w: Fp8WeightT, device) -> Fp8WeightC:
+    _need(w.q, "w.q", torch.float8_e4m3fn, w.q.shape, device)
+    if w.q.dim() != 3:
+        raise ValueError("w.q: expected [E, N, K]")
+    _need(w.scales, "w.scales", torch.float32, (w.E, -(-w.N // 128), -(-w.K // 128)), device)
+    return Fp8WeightC(_p(w.q), _p(w.scales), w.E, w.N, w.K)
+
+
+def _groups_c(routing: Routing, w: Fp8WeightT, device) -> GroupsC:
+    for name, n in (("expert_offsets", w.E + 1), ("active", w.E), ("num_active", 1)):
+        _need(getattr(routing, name), "routing." + name, torch.int32, (n,), device)
+    return routing.groups()
+
+
+def moe_quantize_fp8_rows(x: torch.Tensor, routing: Routing | None = None, stream=None,
+                          out: Fp8Rows | None = None) -> Fp8Rows:
+    """BF16 rows [T, K] to FP8 rows; with a routing, token t is written to its k permuted rows
+    (the grouped product's input, [T*k, K])."""
+    if x.dim() != 2:
+        raise ValueError("x: expected [T, K]")
+    T, K = x.shape
+    dev = x.device
+    _need(x, "x", torch.bfloat16, (T, K))
+    k = 1 if routing is None else routing.k
+    if routing is not None:
+        _need(routing.inv_perm, "routing.inv_perm", torch.int32, (T * k,), dev)
+    with _on(dev, stream):
+        if out is None:
+            out = _new_fp8_rows(T * k, K, dev)
+        else:
+            _need_fp8_rows(out, "out", T * k, K, dev)
+        _check(lib().moe_quantize_fp8_rows(_p(x), T, K, None if routing is None else _p(routing.inv_perm),
+                                           k, _p(out.q), _p(out.scales), _stream()),
+               "moe_quantize_fp8_rows")
+    return out
+
+
+def moe_dequantize_fp8_rows(rows: Fp8Rows, stream=None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """FP8 rows or an 8-bit checkpoint as BF16 [M, K]."""
+    if rows.q.dim() != 2:
+        raise ValueError("rows.q: expected [M, K]")
+    M, K = rows.q.shape
+    dev = rows.q.device
+    _need_fp8_rows(rows, "rows", M, K, dev, rows.fmt == FP8_BLOCK32_E8M0)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        else:
+            _need(out, "out", torch.bfloat16, (M, K), dev)
+        _check(lib().moe_dequantize_fp8_rows(_p(rows.q), _p(rows.scales), M, K, rows.fmt, _p(out),
+                                             _stream()), "moe_dequantize_fp8_rows")
+    return out
+
+
+def moe_grouped_fp8_gemm_fwd(a: Fp8Rows, w: Fp8WeightT, routing: Routing, epi: int = EPI_NONE,
+                             save_gu: bool = False, stream=None):
+    """EPI_NONE: BF16 [M, N]. EPI_SWIGLU: (h as Fp8Rows [M, N/2], the 8-bit checkpoint of
+    gate|up as Fp8Rows [M, N], or None without save_gu)."""
+    if a.q.dim() != 2:
+        raise ValueError("a.q: expected [M, K]")
+    M, dev = a.q.shape[0], a.q.device
+    wc, g = _fp8_weight_c(w, dev), _groups_c(routing, w, dev)
+    _need_fp8_rows(a, "a", M, w.K, dev)
+    if save_gu and epi != EPI_SWIGLU:
+        raise ValueError("save_gu: only with EPI_SWIGLU")
+    with _on(dev, stream):
+        if epi == EPI_SWIGLU:
+            h = _new_fp8_rows(M, w.N // 2, dev)
+            saved = _new_fp8_rows(M, w.N, dev, e8m0=True) if save_gu else None
+            outs = (_p(h.q), _p(h.scales), _p(saved.q) if save_gu else None,
+                    _p(saved.scales) if save_gu else None)
+        else:
+            out = torch.empty((M, w.N), dtype=torch.bfloat16, device=dev)
+            outs = (_p(out), None, None, None)
+        _check(lib().moe_grouped_fp8_gemm_fwd(_p(a.q), _p(a.scales), M, ctypes.byref(wc), ctypes.byref(g),
+                                              epi, *outs, _stream()), "moe_grouped_fp8_gemm_fwd")
+    return (h, saved) if epi == EPI_SWIGLU else out
+
+
+def moe_grouped_fp8_gemm_bwd_dx(dout: Fp8Rows, w: Fp8WeightT, routing: Routing, epi: int = EPI_NONE,
+                                saved: Fp8Rows | None = None, stream=None):
+    """EPI_NONE: din, BF16 [M, K]. EPI_SWIGLU_BWD: [dg | du] as Fp8Rows [M, 2K] from the 8-bit
+    checkpoint `saved` [M, 2K]."""
+    if dout.q.dim() != 2:
+        raise ValueError("dout.q: expected [M, N]")
+    M, dev = dout.q.shape[0], dout.q.device
+    wc, g = _fp8_weight_c(w, dev), _groups_c(routing, w, dev)
+    _need_fp8_rows(dout, "dout", M, w.N, dev)
+    glu = epi == EPI_SWIGLU_BWD
+    if glu != (saved is not None):
+        raise ValueError("saved: exactly with EPI_SWIGLU_BWD")
+    if glu:
+        _need_fp8_rows(saved, "saved", M, 2 * w.K, dev, e8m0=True)
+    with _on(dev, stream):
+        if glu:
+            out = _new_fp8_rows(M, 2 * w.K, dev)
+            outs = (_p(saved.q), _p(saved.scales), _p(out.q), _p(out.scales))
+        else:
+            out = torch.empty((M, w.K), dtype=torch.bfloat16, device=dev)
+            outs = (None, None, _p(out), None)
+        _check(lib().moe_grouped_fp8_gemm_bwd_dx(_p(dout.q), _p(dout.scales), M, ctypes.byref(wc),
+                                                 ctypes.byref(g), epi, *outs, _stream()),
+               "moe_grouped_fp8_gemm_bwd_dx")
+    return out
 
 
 def moe_test_set_wait_budget(cycles: int):

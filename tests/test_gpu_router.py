@@ -1,0 +1,265 @@
+"""moe_route_scored, moe_route_scored_bwd and moe_combine_bwd against their
+float64 definitions.
+
+Tolerances. Gates: a score is an exponential and a division in FP32 (expf:
+2 ulp, division and the sum of at most 1024 positive terms in warp order: 40
+rounding steps at most), so 64 * 2^-24 relative. d_gates: D products summed in
+FP32, every rounding at most 2^-24 of the sum of magnitudes: (D + 16) * 2^-24 *
+sum |dy * row| bounds any order. d_rows: one BF16 rounding, 2^-8 relative.
+d_logits: built from numbers c_i s_i / S with the relative error of the
+scores, 64 * 2^-24 each; the subtraction makes that an error relative to the
+magnitudes |dw| + sum |dw| s / S, as derived beside the check.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import scored_fp8 as O8
+import oracle as O
+from quantized_rl_fine_b200 import moeq
+
+from _common import f64
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+U = 2.0 ** -24
+
+
+def _spec(**kw):
+    return moeq.RouterSpec(**kw)
+
+
+def _check(logits, k, spec, bias=None, x=None, chunk=8, r=None):
+    if r is None:
+        r = moeq.moe_route_scored(logits.to(DEV), None if x is None else x.to(DEV), k, chunk, spec,
+                                  bias=None if bias is None else bias.to(DEV))
+    kw = dict(score=spec.score, groups=spec.groups, topk_groups=spec.topk_groups,
+              group_top=spec.group_top, renorm=spec.renorm, scale=spec.scale)
+    topk, gates = O8.route_scored(logits.numpy(), k, bias=None if bias is None else bias.numpy(), **kw)
+    E = logits.shape[1]
+    assert np.array_equal(r.topk_idx.cpu().numpy(), topk)
+    # 64 rounding steps on every factor of a gate; below 2^-126 absolute
+    assert np.all(np.abs(f64(r.gates) - gates) <= 64 * U * np.abs(gates) + 2.0 ** -126)
+    g = O.group_by_expert(topk, E, chunk)
+    A, nch = int(r.num_active.item()), int(r.num_chunks.item())
+    assert np.array_equal(r.expert_offsets.cpu().numpy(), g.offsets)
+    assert A == g.num_active and nch == g.num_chunks
+    assert np.array_equal(r.active.cpu().numpy()[:A], g.active)
+    assert np.array_equal(r.chunk_offsets.cpu().numpy()[:nch + 1], g.chunk_offsets)
+    assert np.array_equal(r.perm_token.cpu().numpy(), g.perm_token)
+    assert np.array_equal(r.inv_perm.cpu().numpy(), g.inv_perm)
+    if x is not None:
+        xp = r.x_perm.cpu().view(torch.int16).numpy()
+        assert np.array_equal(xp, x.view(torch.int16).numpy()[g.perm_token])
+    return r, topk
+
+
+CASES = [
+    # T, E, k, spec, bias
+    (1, 1, 1, dict(score="softmax"), False),
+    (1, 384, 8, dict(score="sigmoid", groups=8, topk_groups=4, group_top=2, scale=2.5), True),
+    (37, 5, 3, dict(score="softmax", renorm=False), False),
+    (64, 8, 2, dict(score="sigmoid", renorm=False, scale=0.5), True),
+    (130, 384, 8, dict(score="softmax", groups=8, topk_groups=3, group_top=1), False),
+    (100, 160, 6, dict(score="softmax", groups=8, topk_groups=3, group_top=1, renorm=False), False),
+    (257, 64, 32, dict(score="sigmoid", groups=2, topk_groups=1, group_top=2), False),
+    (33, 96, 4, dict(score="sigmoid", groups=32, topk_groups=2, group_top=2), True),
+    (90, 21, 3, dict(score="softmax", groups=7, topk_groups=1, group_top=2), True),
+    (40, 12, 12, dict(score="sigmoid", groups=3, topk_groups=3, group_top=2), True),
+    (1500, 256, 8, dict(score="sigmoid", groups=8, topk_groups=4, group_top=2, scale=2.5), True),
+    (1100, 48, 4, dict(score="softmax", groups=6, topk_groups=2, group_top=1), True),
+    (65, 1024, 8, dict(score="sigmoid", groups=16, topk_groups=4, group_top=2), True),
+    (50, 1000, 5, dict(score="softmax", renorm=False), True),
+]
+
+
+@pytest.mark.parametrize("T,E,k,kw,with_bias", CASES)
+def test_route_scored_against_definition(T, E, k, kw, with_bias):
+    g = torch.Generator().manual_seed(T * 31 + E)
+    logits = torch.randn((T, E), generator=g)
+    bias = 0.1 * torch.randn(E, generator=g) if with_bias else None
+    x = torch.randn((T, 24), generator=g).to(torch.bfloat16)
+    _check(logits, k, _spec(**kw), bias, x)
+
+
+@pytest.mark.parametrize("T,E,k,kw,with_bias", CASES[1:])
+def test_exact_ties_go_to_the_lower_id(T, E, k, kw, with_bias):
+    """Few distinct logits and biases: most selections and groups are decided by ties."""
+    g = torch.Generator().manual_seed(T + 7 * E)
+    logits = torch.randint(-1, 2, (T, E), generator=g).float()
+    bias = torch.randint(0, 2, (E,), generator=g).float() if with_bias else None
+    _check(logits, k, _spec(**kw), bias)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,topk_groups,group_top", [(1, 1, 1), (4, 2, 1), (4, 2, 2)])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_masked_experts(score, groups, topk_groups, group_top, with_bias):
+    T, E, k = 70, 24, 6
+    g = torch.Generator().manual_seed(5)
+    logits = torch.randn((T, E), generator=g)
+    logits[0] = -float("inf")                                # nothing left
+    logits[1, 1:] = -float("inf")                            # one expert left
+    logits[2] = float("nan")
+    logits[3, ::2] = float("nan")
+    logits[4, :20] = -float("inf")                           # fewer than k left in one group
+    logits[5] = torch.finfo(torch.float32).min               # the type's lowest value is a number
+    logits[6, 3:] = torch.finfo(torch.float32).min
+    logits[7, 5] = float("inf")
+    logits[8] = -200.0                                       # sigmoid underflows in FP32
+    logits[9, :] = 60.0                                      # sigmoid saturates
+    logits[9, 7] = 90.0
+    logits[10:40][torch.rand((30, E), generator=g) < 0.6] = -float("inf")
+    bias = 0.1 * torch.randn(E, generator=g) if with_bias else None
+    if with_bias:
+        bias[2], bias[9] = -float("inf"), float("nan")
+    spec = _spec(score=score, groups=groups, topk_groups=topk_groups, group_top=group_top)
+    r, topk = _check(logits, k, spec, bias)
+    assert all(len(set(row)) == k for row in r.topk_idx.cpu().tolist())
+    d = moeq.moe_route_scored_bwd(torch.ones((T, k), device=DEV), logits.to(DEV), r, spec)
+    assert torch.isfinite(d).all()
+    assert not d.cpu()[0].any() and not d.cpu()[2].any()
+
+
+def test_keys_that_differ_below_single_precision():
+    """Scores closer than FP32 resolves: the order is the one of the 64-bit keys."""
+    E, k = 64, 8
+    g = torch.Generator().manual_seed(3)
+    bias = torch.zeros(E)
+    # logits one FP32 step apart around 12: their sigmoids differ by 1e-11
+    base = torch.full((E,), 12.0)
+    step = torch.nextafter(base, torch.full((E,), 100.0)) - base
+    logits = torch.stack([base + step * torch.randperm(E, generator=g).float() for _ in range(40)])
+    for spec in (_spec(score="sigmoid"), _spec(score="softmax"),
+                 _spec(score="sigmoid", groups=8, topk_groups=4, group_top=2)):
+        _check(logits, k, spec, bias)
+        _check(logits, k, spec, None)
+    # bias and score that cancel: keys near 0 from numbers near 0.5
+    bias = -torch.sigmoid(torch.linspace(-1, 1, E))
+    logits = torch.linspace(-1, 1, E).repeat(20, 1) + 1e-6 * torch.randn((20, E), generator=g)
+    _check(logits, k, _spec(score="sigmoid"), bias)
+
+
+@pytest.mark.parametrize("T,E,k,score,renorm,scale", [
+    (1, 1, 1, "softmax", False, 1.0), (1, 384, 8, "sigmoid", True, 2.5),
+    (131, 64, 4, "softmax", False, 1.0), (77, 21, 5, "softmax", True, 1.5),
+    (300, 1000, 32, "sigmoid", False, 2.5), (64, 100, 2, "sigmoid", True, 1.0)])
+def test_router_gradient(T, E, k, score, renorm, scale):
+    g = torch.Generator().manual_seed(T + E)
+    logits = 2 * torch.randn((T, E), generator=g)
+    dg = torch.randn((T, k), generator=g)
+    spec = _spec(score=score, renorm=renorm, scale=scale)
+    r = moeq.moe_route_scored(logits.to(DEV), None, k, 8, spec)
+    out = torch.full((T, E), float("nan"), device=DEV)
+    got = f64(moeq.moe_route_scored_bwd(dg.to(DEV), logits.to(DEV), r, spec, out=out))
+    topk = r.topk_idx.cpu().numpy()
+    want = O8.route_scored_bwd(dg.numpy(), logits.numpy(), topk, score, renorm, scale)
+    # Magnitudes of what is subtracted: with n = |dw_j| + sum |dw| s / S (over S for
+    # renorm) an error of 64 U of every s moves ds by at most 128 U * n, and the
+    # result by s * (that + the 64 U of s itself on |ds|), the softmax term likewise.
+    s = O8.scored_scores(logits.numpy(), score)
+    w = np.take_along_axis(s, topk.astype(np.int64), 1)
+    dw = np.abs(scale * dg.numpy().astype(np.float64))
+    if renorm:
+        S = w.sum(1, keepdims=True)
+        n = (dw + (dw * w).sum(1, keepdims=True) / S) / S
+    else:
+        n = dw
+    full = np.zeros((T, E))
+    np.put_along_axis(full, topk.astype(np.int64), n, 1)
+    lim = s * full
+    if score == "softmax":
+        lim = lim + s * (full * s).sum(1, keepdims=True)
+    assert np.all(np.abs(got - want) <= 256 * U * lim + 2.0 ** -120)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_router_gradient_against_differences(score, renorm):
+    """The definition's own gates, moved by small steps of the logits, in float64."""
+    T, E, k, h = 6, 12, 3, 1e-5
+    g = torch.Generator().manual_seed(9)
+    logits = torch.randn((T, E), generator=g)
+    dg = torch.randn((T, k), generator=g)
+    spec = _spec(score=score, renorm=renorm, scale=1.5)
+    r = moeq.moe_route_scored(logits.to(DEV), None, k, 8, spec)
+    got = f64(moeq.moe_route_scored_bwd(dg.to(DEV), logits.to(DEV), r, spec))
+    idx = r.topk_idx.cpu().numpy().astype(np.int64)
+
+    def loss(x):
+        s = O8.scored_scores(x, score)
+        w = np.take_along_axis(s, idx, 1)
+        if renorm:
+            w = w / w.sum(1, keepdims=True)
+        return (1.5 * w * dg.numpy().astype(np.float64)).sum(1)
+
+    x = f64(logits)
+    num = np.zeros((T, E))
+    for e in range(E):
+        d = np.zeros((1, E))
+        d[0, e] = h
+        num[:, e] = (loss(x + d) - loss(x - d)) / (2 * h)
+    # second-order differences of functions with derivatives of order one: h^2, and FP32 results
+    assert np.abs(got - num).max() <= 10 * h * h + 256 * U * np.abs(dg.numpy()).sum(1).max() * 1.5
+
+
+@pytest.mark.parametrize("T,E,k,D,with_gates", [(1, 4, 1, 8, True), (5, 8, 3, 72, True),
+                                                (131, 64, 4, 2048, True), (33, 40, 32, 264, True),
+                                                (64, 12, 9, 4104, False), (20, 32, 16, 7168, True)])
+def test_combine_bwd(T, E, k, D, with_gates):
+    g = torch.Generator().manual_seed(T + D)
+    logits = torch.randn((T, E), generator=g)
+    dy = torch.randn((T, D), generator=g).to(torch.bfloat16)
+    rows = torch.randn((T * k, D), generator=g).to(torch.bfloat16)
+    r = moeq.moe_route_scored(logits.to(DEV), None, k, 8, _spec())
+    if not with_gates:
+        r.gates = None
+    out = torch.full((T * k, D), float("nan"), dtype=torch.bfloat16, device=DEV)
+    d_rows, d_gates = moeq.moe_combine_bwd(dy.to(DEV), rows.to(DEV), r, out=out)
+    inv = r.inv_perm.cpu().numpy()
+    gates = None if r.gates is None else f64(r.gates)
+    wr, wg = O8.combine_bwd(f64(dy), f64(rows), inv, gates, k)
+    mag = np.stack([[np.abs(f64(dy[t]) * f64(rows[int(inv[t * k + j])])).sum() for j in range(k)]
+                    for t in range(T)])
+    assert np.all(np.abs(f64(d_gates) - wg) <= (D + 16) * U * mag)
+    assert np.all(np.abs(f64(d_rows) - wr) <= 2.0 ** -8 * np.abs(wr))
+    # the same bits as the existing scatter
+    assert torch.equal(d_rows, moeq.moe_unpermute_combine(dy.to(DEV), r, r.gates, T, mode=1))
+    again = moeq.moe_combine_bwd(dy.to(DEV), rows.to(DEV), r)
+    assert torch.equal(again[0], d_rows) and torch.equal(again[1], d_gates)
+
+
+def test_router_chain_captured_and_on_another_stream():
+    """Forward, combine backward and router backward captured into a graph and replayed with
+    new inputs, and the same calls on a stream of their own."""
+    T, E, k, D = 1200, 64, 4, 64
+    spec = _spec(score="sigmoid", groups=4, topk_groups=2, group_top=2)
+    g = torch.Generator().manual_seed(1)
+    sets = [(torch.randn((T, E), generator=g).to(DEV), torch.randn((T, D), generator=g).to(torch.bfloat16).to(DEV),
+             torch.randn((T * k, D), generator=g).to(torch.bfloat16).to(DEV)) for _ in range(2)]
+    bias = (0.1 * torch.randn(E, generator=g)).to(DEV)
+
+    def chain(lg, dy, rows, stream=None):
+        r = moeq.moe_route_scored(lg, None, k, 8, spec, bias=bias, stream=stream)
+        d_rows, d_gates = moeq.moe_combine_bwd(dy, rows, r, stream=stream)
+        return r.topk_idx, r.gates, d_rows, d_gates, moeq.moe_route_scored_bwd(d_gates, lg, r, spec, stream=stream)
+
+    want = [[t.clone() for t in chain(*s)] for s in sets]
+    lg, dy, rows = (t.clone() for t in sets[0])
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        outs = chain(lg, dy, rows)
+    for s, w in zip(sets[::-1], want[::-1]):
+        for dst, src in zip((lg, dy, rows), s):
+            dst.copy_(src)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, w))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = chain(*sets[1], stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want[1]))
