@@ -517,6 +517,8 @@ moe_status run_fp8_gemm(bool bwd, int epi, const void* rows, const float* row_sc
   const int F = bwd ? w->K : (epi == MOE_EPI_SWIGLU ? w->N / 2 : w->N);
   const int tile_f = (!bwd && epi == MOE_EPI_SWIGLU) ? 128 : 256;
   CUtensorMap ta, tw;
+  bool pair = M > 256 * static_cast<int64_t>(w->E);
+  if (const char* env = getenv("MOEQ_F8PAIR")) pair = atoi(env) == 1;
   // Rows and weights as boxes of 128 bytes x 128 rows, 128-byte swizzle; what
   // lies past the reduction length, the features or the rows reads as zeros.
   const uint64_t N = w->N, K = w->K, E = w->E, rl = R;
@@ -538,6 +540,9 @@ moe_status run_fp8_gemm(bool bwd, int epi, const void* rows, const float* row_sc
   p.M = static_cast<int32_t>(M);
   p.R = R;
   p.n_ftiles = (F + tile_f - 1) / tile_f;
+  p.nkb = (R + 127) / 128;
+  p.NB = (w->N + 127) / 128;
+  p.KB = (w->K + 127) / 128;
   p.a_scales = row_scales;
   p.w_scales = w->scales;
   p.out = static_cast<uint8_t*>(out);
@@ -547,8 +552,10 @@ moe_status run_fp8_gemm(bool bwd, int epi, const void* rows, const float* row_sc
   // the most tiles that M rows over E experts can make; the list is 32-bit
   const int64_t bound = static_cast<int64_t>(p.n_ftiles) * (std::min<int64_t>(w->E, M) + M / 128 + 1);
   if (bound >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
-  const int grid = static_cast<int>(std::min<int64_t>(num_sms(), bound));
-  return cuda_status(launch_grouped_fp8_gemm(bwd, epi, ta, tw, p, grid, s));
+  int64_t ctas = std::min<int64_t>(num_sms(), bound);
+  if (pair) ctas = std::max<int64_t>(2, std::min<int64_t>(num_sms(), 2 * bound) / 2 * 2);
+  return cuda_status(
+      launch_grouped_fp8_gemm(bwd, epi, ta, tw, p, pair, static_cast<int>(ctas), s));
 }
 
 // Checks shared by the two FP8 products.

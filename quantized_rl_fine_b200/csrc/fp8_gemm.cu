@@ -25,6 +25,7 @@
 // its copies and MMAs in flight finish (again bounded), frees tensor memory
 // and returns.
 #include <algorithm>
+#include <atomic>
 
 #include "fp8.cuh"
 #include "fp8_gemm.cuh"
@@ -35,8 +36,9 @@ namespace {
 
 constexpr int kRows8 = 128;              // token rows per tile (MMA M)
 constexpr uint32_t kBoxBytes = 16384;    // one operand box: 128 rows x 128 bytes
-constexpr uint32_t kStage8 = 3 * kBoxBytes;
-constexpr int kStages8 = 3;
+// One stage: the CTA's token rows and two weight boxes (one in a pair).
+__host__ __device__ constexpr uint32_t stage_bytes8(int pair) { return (pair ? 2u : 3u) * kBoxBytes; }
+__host__ __device__ constexpr int stages8(int pair) { return pair ? 4 : 3; }
 constexpr int kEpiWarp8 = 4;             // warp 0 copies, warp 1 issues MMAs, warps 4-11 epilogue
 constexpr int kEpiWarps8 = 8;
 constexpr int kThreads8 = 32 * (kEpiWarp8 + kEpiWarps8);
@@ -48,11 +50,11 @@ static_assert(128 * kRegsCopy + 256 * kRegsEpi <= kThreads8 * 168, "register spl
 // Output staging of one epilogue thread: its 256 bytes of a row, padded so
 // that the 16-byte stores of eight neighbouring threads fall in distinct banks.
 constexpr uint32_t kSlot8 = 272;
-constexpr size_t smem_bytes8(int E) {
-  return 1024 + kStages8 * kStage8 + 256 * kSlot8 + 8 * (2 * kStages8 + 8) + 16 + 4 * 4 * kRows8 + 4 * 32 +
+constexpr size_t smem_bytes8(int E, int pair) {
+  return 1024 + stages8(pair) * stage_bytes8(pair) + 256 * kSlot8 + 8 * (2 * stages8(pair) + 8) + 16 + 4 * 4 * kRows8 + 4 * 32 +
          4 * 2 * (static_cast<size_t>(E) + 1) + 2 * static_cast<size_t>(E);
 }
-static_assert(smem_bytes8(1024) <= 227 * 1024, "shared memory of the largest stack");
+static_assert(smem_bytes8(1024, 0) <= 227 * 1024 && smem_bytes8(1024, 1) <= 227 * 1024, "shared memory of the largest stack");
 
 // D[tmem] (+)= A[smem] * B[smem]^T, e4m3 in, FP32 accumulation, K = 32.
 __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
@@ -63,6 +65,60 @@ __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// The same over a pair: D and A 128 rows in each CTA, B's N rows split between
+// them (even CTA [0, N/2)), M = 256.
+__device__ __forceinline__ void mma_f8_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                               uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, {%5, %5, %5, %5, %5, %5, %5, %5}, p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(0u)
+      : "memory");
+}
+
+// 128 x 128 byte box; in a pair `bar` may be the other CTA's barrier (a
+// cluster address). No multicast: each CTA brings its own boxes.
+template <int PAIR>
+__device__ __forceinline__ void tma_load8(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0,
+                                          int32_t c1, int32_t c2, uint64_t policy) {
+  if constexpr (PAIR) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
+        : "memory");
+  } else {
+    tma_load_3d_hint(dst, map, bar, c0, c1, c2, policy);
+  }
+}
+
+// Arrival on the other CTA's barrier with the default (CTA) release: what it
+// hands over is tensor memory, ordered by the tcgen05 fence before it. A
+// cluster-scope release here, or a cluster-scope acquire in the wait, cost
+// 1.5 us per reduction block (the product 2.2x slower).
+__device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+// mbar_wait with few registers held: 32-bit clock, the abort flag by its
+// shared-memory address, the budget (2^32 - 1 cycles at most) read when asked.
+__device__ __forceinline__ bool mbar_wait8(uint32_t bar, uint32_t parity, uint32_t abort_flag) {
+  if (mbar_try_wait_sleep(bar, parity, kWaitSleepNs)) return true;
+  const uint32_t t0 = static_cast<uint32_t>(clock());
+  while (!mbar_try_wait_sleep(bar, parity, kWaitSleepNs)) {
+    uint32_t gone;
+    asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(gone) : "r"(abort_flag));
+    if (gone) return false;
+    if (static_cast<uint32_t>(clock()) - t0 > *reinterpret_cast<volatile long long*>(&g_wait_budget)) {
+      raise_device_error(MOE_DEVERR_WAIT_TIMEOUT);
+      asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort_flag), "r"(1u));
+      return false;
+    }
+  }
+  return true;
 }
 
 // Instruction descriptor, kind::f8f6f4: FP32 D, e4m3 A and B (format 0).
@@ -86,7 +142,9 @@ struct Tile8 {
 // Tile t (a0: active index of an earlier tile): feature tile major, token tile
 // minor inside an expert, experts in active order, so the tiles in flight
 // share weights first.
-__device__ __forceinline__ Tile8 tile8_at(const TileList8& tl, int t, int a0) {
+template <int PAIR>
+__device__ __forceinline__ Tile8 tile8_at(const TileList8& tl, int t, int a0, int rank) {
+  constexpr int kTileRows = kRows8 << PAIR;
   int lo = a0, hi = tl.A - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -96,10 +154,10 @@ __device__ __forceinline__ Tile8 tile8_at(const TileList8& tl, int t, int a0) {
   r.a = lo;
   r.e = tl.id[lo];
   const int seg0 = tl.seg[lo], seg1 = tl.seg[lo + 1];
-  const int nrt = (seg1 - seg0 + kRows8 - 1) / kRows8;
+  const int nrt = (seg1 - seg0 + kTileRows - 1) / kTileRows;
   const int local = t - tl.start[lo];
   r.ft = local / nrt;
-  r.row0 = seg0 + (local - r.ft * nrt) * kRows8;
+  r.row0 = seg0 + (local - r.ft * nrt) * kTileRows + rank * kRows8;
   r.row_end = min(seg1, r.row0 + kRows8);
   return r;
 }
@@ -107,7 +165,9 @@ __device__ __forceinline__ Tile8 tile8_at(const TileList8& tl, int t, int a0) {
 // Builds the list; the active experts' rows must lie behind one another from
 // 0 to M. Tables that do not say so (or name an expert outside the stack) give
 // an empty list and the device error.
+template <int PAIR>
 __device__ void build_tiles8(const Fp8GemmArgs& p, TileList8& tl, int32_t* warp_tot) {
+  constexpr int kTileRows = kRows8 << PAIR;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, nw = blockDim.x >> 5;
   const int A_raw = *p.num_active;
   bool bad = !(A_raw >= 1 && A_raw <= p.E && p.offsets[0] == 0 && p.offsets[p.E] == p.M);
@@ -127,7 +187,7 @@ __device__ void build_tiles8(const Fp8GemmArgs& p, TileList8& tl, int32_t* warp_
     }
     tl.seg[a] = s0;
     tl.id[a] = static_cast<uint16_t>(e);
-    local += p.n_ftiles * ((s1 - s0 + kRows8 - 1) / kRows8);
+    local += p.n_ftiles * ((s1 - s0 + kTileRows - 1) / kTileRows);
   }
   if (__syncthreads_or(bad ? 1 : 0)) {
     if (tid == 0) {
@@ -151,7 +211,7 @@ __device__ void build_tiles8(const Fp8GemmArgs& p, TileList8& tl, int32_t* warp_
   for (int i = 0; i < w; ++i) run += warp_tot[i];
   for (int a = a0; a < a1; ++a) {
     tl.start[a] = run;
-    run += p.n_ftiles * ((tl.seg[a + 1] - tl.seg[a] + kRows8 - 1) / kRows8);
+    run += p.n_ftiles * ((tl.seg[a + 1] - tl.seg[a] + kTileRows - 1) / kTileRows);
   }
   if (tid == 0) {
     int total = 0;
@@ -268,7 +328,7 @@ __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-template <int BWD, int EPI>
+template <int BWD, int EPI, int PAIR>
 __global__ void __launch_bounds__(kThreads8, 1)
 grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
                         const __grid_constant__ CUtensorMap tm_w, const Fp8GemmArgs p) {
@@ -278,14 +338,15 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
   const uint32_t raw = smem_u32(smem_raw8);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw8 + (base - raw);
-  constexpr int S = kStages8;
+  constexpr int S = stages8(PAIR);
+  constexpr uint32_t kStage8 = stage_bytes8(PAIR);
   auto A_at = [&](int s) { return base + s * kStage8; };
   auto B_at = [&](int s) { return base + s * kStage8 + kBoxBytes; };
   const uint32_t stg_base = base + S * kStage8;
   const uint32_t bars = stg_base + 256 * kSlot8;
   auto full = [&](int s) { return bars + 8u * s; };
   auto empty = [&](int s) { return bars + 8u * (S + s); };
-  auto acc_full = [&](int b) { return bars + 8u * (2 * S + b); };
+  auto acc_full = [&](int b) { return bars + 8u * (2 * S + b); };      // accumulator buffer b (two)
   auto acc_empty = [&](int b) { return bars + 8u * (2 * S + 2 + b); };
   const uint32_t drain_bar = bars + 8u * (2 * S + 4);
   const uint32_t amax_bar = bars + 8u * (2 * S + 5);
@@ -293,6 +354,7 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
   const uint32_t slot_free = bars + 8u * (2 * S + 7);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (bars - base) + 8u * (2 * S + 8));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const uint32_t abort_at = bars + 8u * (2 * S + 8) + 4u;
   float* row_amax = reinterpret_cast<float*>(tmem_slot + 4);                 // [2 tiles][2][128]
   int32_t* warp_tot = reinterpret_cast<int32_t*>(row_amax + 4 * kRows8);     // [32]
   TileList8 list;
@@ -301,6 +363,10 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
   list.id = reinterpret_cast<uint16_t*>(list.seg + p.E + 1);                 // [E]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // Position in the pair (0 issues the MMAs) and the tile walk.
+  const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+  const int t_first = static_cast<int>(blockIdx.x) >> PAIR;
+  const int t_step = static_cast<int>(gridDim.x) >> PAIR;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full(s), 1);
@@ -308,7 +374,7 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full(b), 1);
-      mbar_init(acc_empty(b), kEpiWarps8);
+      mbar_init(acc_empty(b), kEpiWarps8 << PAIR);
     }
     mbar_init(drain_bar, 1);
     mbar_init(amax_bar, kEpiWarps8);
@@ -319,17 +385,21 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
     tma_prefetch_desc(&tm_a);
     tma_prefetch_desc(&tm_w);
   }
-  if (warp == 1) tmem_alloc(smem_u32(tmem_slot), 512);
+  if (warp == 1) {
+    if constexpr (PAIR) tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    else tmem_alloc(smem_u32(tmem_slot), 512);
+  }
   tc_fence_before();
-  __syncthreads();
+  // (a pair also waits until the other CTA's barriers are initialised)
+  if constexpr (PAIR) cluster_sync_all(); else __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   grid_dependency_wait();
   grid_dependents_launch();
 
-  build_tiles8(p, list, warp_tot);
+  build_tiles8<PAIR>(p, list, warp_tot);
   const int total = list.start[list.A];
-  const int nkb = (p.R + 127) / 128;      // blocks of the reduction
+  const int nkb = p.nkb;                  // blocks of the reduction
   const int f_half = p.N >> 1;            // SwiGLU: first up row
 
   if (warp < kEpiWarp8) {
@@ -345,49 +415,57 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
       bool ok = true;
       Tile8 tl;
       tl.a = 0;
-      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-        tl = tile8_at(list, t, tl.a);
+      for (int t = t_first; t < total && ok; t += t_step) {
+        tl = tile8_at<PAIR>(list, t, tl.a, rank);
         const int c0 = kGlu ? tl.ft * 128 : tl.ft * 256;       // features of the two boxes
         const int c1 = kGlu ? f_half + tl.ft * 128 : c0 + 128;
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait(empty(st), ph ^ 1u, abort_flag)) { ok = false; break; }
-          const uint32_t bar = full(st);
-          mbar_arrive_expect_tx(bar, kStage8);
-          tma_load_3d_hint(A_at(st), &tm_a, bar, kb * 128, tl.row0, 0, pol_a);
+          if (!mbar_wait8(empty(st), ph ^ 1u, abort_at)) { ok = false; break; }
+          // A pair's stages are one: both CTAs' copies count on the even CTA's
+          // barrier, which is where the MMAs are issued.
+          uint32_t bar = full(st);
+          if constexpr (PAIR) bar = cluster_addr(bar, 0);
+          if (rank == 0) mbar_arrive_expect_tx(full(st), kStage8 << PAIR);
+          tma_load8<PAIR>(A_at(st), &tm_a, bar, kb * 128, tl.row0, 0, pol_a);
+          // weight boxes: both, or in a pair the CTA's own half of the features
+          const int cf = rank == 1 ? c1 : c0;
           if constexpr (BWD) {
-            tma_load_3d_hint(B_at(st), &tm_w, bar, c0, kb * 128, tl.e, pol_w);
-            tma_load_3d_hint(B_at(st) + kBoxBytes, &tm_w, bar, c1, kb * 128, tl.e, pol_w);
+            tma_load8<PAIR>(B_at(st), &tm_w, bar, cf, kb * 128, tl.e, pol_w);
+            if constexpr (!PAIR) tma_load8<PAIR>(B_at(st) + kBoxBytes, &tm_w, bar, c1, kb * 128, tl.e, pol_w);
           } else {
-            tma_load_3d_hint(B_at(st), &tm_w, bar, kb * 128, c0, tl.e, pol_w);
-            tma_load_3d_hint(B_at(st) + kBoxBytes, &tm_w, bar, kb * 128, c1, tl.e, pol_w);
+            tma_load8<PAIR>(B_at(st), &tm_w, bar, kb * 128, cf, tl.e, pol_w);
+            if constexpr (!PAIR) tma_load8<PAIR>(B_at(st) + kBoxBytes, &tm_w, bar, kb * 128, c1, tl.e, pol_w);
           }
           ++issued;
           if (++st == S) { st = 0; ph ^= 1u; }
         }
       }
-      if (!ok) {
-        // copies in flight land before the CTA can exit
+      if (!ok && rank == 0) {
+        // Copies in flight (a pair's odd CTA's too) land before the CTAs can exit.
         for (long long g = issued > S ? issued - S : 0; g < issued; ++g)
           mbar_drain(full(static_cast<int>(g % S)), static_cast<uint32_t>((g / S) & 1));
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == 1 && rank == 0) {
     // ------------------------------------------------------------ MMA issuer
-    constexpr uint32_t idesc = idesc_f8(kRows8, 256, BWD ? 1u : 0u);
+    constexpr uint32_t idesc = idesc_f8(kRows8 << PAIR, 256, BWD ? 1u : 0u);
     int st = 0;
     uint32_t ph = 0;
-    long long it = 0;                     // reduction blocks handed over (buffer it % 2)
+    uint32_t it = 0;                      // reduction blocks handed over (buffer it % 2)
     bool ok = true;
     auto wait_w = [&](uint32_t bar, uint32_t parity) {
-      const bool r = mbar_wait(bar, parity, abort_flag);
+      const bool r = mbar_wait8(bar, parity, abort_at);
       return __shfl_sync(0xffffffffu, r ? 1 : 0, 0) != 0;
     };
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+    auto commit = [](uint32_t bar) {
+      if constexpr (PAIR) mma_commit_pair(bar, 3); else mma_commit(bar);
+    };
+    for (int t = t_first; t < total && ok; t += t_step) {
       for (int kb = 0; kb < nkb; ++kb, ++it) {
         const int b = static_cast<int>(it & 1);
-        if (!wait_w(acc_empty(b), static_cast<uint32_t>((it >> 1) & 1) ^ 1u)) { ok = false; break; }
         if (!wait_w(full(st), ph)) { ok = false; break; }
+        if (!wait_w(acc_empty(b), static_cast<uint32_t>((it >> 1) & 1) ^ 1u)) { ok = false; break; }
         tc_fence_after();
         if (elect_one()) {
           const uint32_t d = tmem_base + static_cast<uint32_t>(b) * 256u;
@@ -395,16 +473,19 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
           const uint64_t db = BWD ? smem_desc_sw128(B_at(st), kBoxBytes, 1024)
                                   : smem_desc_sw128(B_at(st), 16, 1024);
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)   // 32 of the 128 reduction elements each
-            mma_f8_ss(d, da + 2 * ks, db + (BWD ? 256 : 2) * ks, idesc, ks > 0 ? 1u : 0u);
-          mma_commit(empty(st));
-          mma_commit(acc_full(b));
+          for (int ks = 0; ks < 4; ++ks) {  // 32 of the 128 reduction elements each
+            const uint64_t bk = db + (BWD ? 256 : 2) * ks;
+            if constexpr (PAIR) mma_f8_ss_pair(d, da + 2 * ks, bk, idesc, ks > 0 ? 1u : 0u);
+            else mma_f8_ss(d, da + 2 * ks, bk, idesc, ks > 0 ? 1u : 0u);
+          }
+          commit(empty(st));
+          commit(acc_full(b));
         }
         __syncwarp();
         if (++st == S) { st = 0; ph ^= 1u; }
       }
     }
-    if (elect_one()) mma_commit(drain_bar);
+    if (elect_one()) commit(drain_bar);
     __syncwarp();
     if (lane == 0) mbar_drain(drain_bar, 0);
     __syncwarp();
@@ -416,9 +497,9 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
     int li = 0;
     Tile8 tl;
     tl.a = 0;
-    for (int t = blockIdx.x; t < total; t += gridDim.x, ++li) {
-      tl = tile8_at(list, t, tl.a);
-      ok = mbar_wait(slot_free, static_cast<uint32_t>(li & 1), abort_flag);
+    for (int t = t_first; t < total; t += t_step, ++li) {
+      tl = tile8_at<PAIR>(list, t, tl.a, rank);
+      ok = mbar_wait8(slot_free, static_cast<uint32_t>(li & 1), abort_at);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       uint32_t valid = 0;
@@ -462,93 +543,102 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
     const uint32_t slot = stg_base + static_cast<uint32_t>(threadIdx.x - 32 * kEpiWarp8) * kSlot8;
     // This thread's 128 columns in two halves of 64: plain, one box; SwiGLU,
     // 64 gate columns and the 64 matching up columns.
-    const uint32_t col0 = kGlu ? static_cast<uint32_t>(wg * 64) : static_cast<uint32_t>(wg * 128);
-    const uint32_t col1 = kGlu ? 128u + static_cast<uint32_t>(wg * 64) : col0 + 64u;
-    const int KB = (p.K + 127) / 128, NB = (p.N + 127) / 128;
-    const int w_step = BWD ? KB : 1;             // weight scales of consecutive reduction blocks
-    // Where a tile's scales are: the row's (stride M) and, for the two column
-    // halves, the weight blocks' (stride w_step). Blocks past the last feature
-    // (a tile that ends early) are clamped; their columns are not stored.
-    struct Scales {
-      const float *a, *w0, *w1;
-    };
-    auto scales_of = [&](const Tile8& tl) {
-      const float* swe = p.w_scales + static_cast<int64_t>(tl.e) * NB * KB;
-      const int b0 = kGlu ? tl.ft : min(tl.ft * 2 + wg, (BWD ? KB : NB) - 1);
-      const int b1 = kGlu ? f_half / 128 + tl.ft : b0;
-      return Scales{p.a_scales + min(tl.row0 + r_in, p.M - 1),
-                    BWD ? swe + b0 : swe + static_cast<int64_t>(b0) * KB,
-                    BWD ? swe + b1 : swe + static_cast<int64_t>(b1) * KB};
-    };
-    long long it = 0;
-    int li = 0;                                  // this CTA's tile count
-    Tile8 tl;
-    Scales sc;
+    const uint32_t col0 = static_cast<uint32_t>(kGlu ? wg * 64 : wg * 128);
+    const uint32_t col1 = col0 + (kGlu ? 128u : 64u);
+    // Registers are what this loop is short of (128 accumulators, 64 values in
+    // flight, 232 a thread), and a spill in it costs more than anything else
+    // here, so its state is few words: the tile as (row or -1, ft, a), and
+    // pointers that step through the scales of the reduction blocks: the row's
+    // (stride M) and the weight blocks' of the two column halves (stride
+    // w_step; SwiGLU's up block w_up further on).
+    const int64_t w_up = static_cast<int64_t>(f_half / 128) * p.KB;
+    const float* pa;
+    const float* pw;
+    int row, ft, ta = 0;
     float na = 0.0f, n0 = 0.0f, n1 = 0.0f;       // scales of the next reduction block
-    if (static_cast<int>(blockIdx.x) < total) {
-      tl = tile8_at(list, blockIdx.x, 0);
-      sc = scales_of(tl);
-      na = __ldg(sc.a);
-      n0 = __ldg(sc.w0);
-      if constexpr (kGlu) n1 = __ldg(sc.w1);
+    // Blocks past the last feature (a tile that ends early) are clamped; their
+    // columns are not stored.
+    auto enter = [&](int t) {
+      const Tile8 tl = tile8_at<PAIR>(list, t, ta, rank);
+      ta = tl.a;
+      ft = tl.ft;
+      row = tl.row0 + r_in;
+      pa = p.a_scales + min(row, p.M - 1);
+      if (row >= tl.row_end) row = -1;
+      pw = p.w_scales + static_cast<int64_t>(tl.e) * p.NB * p.KB;
+      if constexpr (BWD) pw += min(ft * 2 + wg, p.KB - 1);
+      else pw += static_cast<int64_t>(kGlu ? ft : min(ft * 2 + wg, p.NB - 1)) * p.KB;
+    };
+    auto fetch = [&]() {
+      na = __ldg(pa);
+      n0 = __ldg(pw);
+      if constexpr (kGlu) n1 = __ldg(pw + w_up);
+      pa += p.M;
+      pw += BWD ? p.KB : 1;
+    };
+    uint32_t it = 0;                             // reduction blocks so far (buffer it % 2)
+    uint32_t li = 0;                             // parity of this CTA's tile count
+    if (t_first < total) {
+      enter(t_first);
+      fetch();
     }
-    for (int t = blockIdx.x; t < total; t += gridDim.x, ++li) {
-      const int row = tl.row0 + r_in;
-      const bool row_ok = row < tl.row_end;
-      const int ft = tl.ft;
+    for (int t = t_first; t < total; t += t_step, li ^= 1u) {
+      const int cur_row = row, cur_ft = ft;
       uint64_t acc2[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc2[j] = 0ull;
       bool ok = true;
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
+      for (int kb = 0; kb < p.nkb; ++kb, ++it) {
         if constexpr (kGluBwd) {
           // Once the previous tile's output has left the staging slots, warp 3
           // brings this tile's g and u there while the product runs.
-          if (kb == min(2, nkb - 1)) {
+          if (kb == min(2, p.nkb - 1)) {
             bulk_wait_read();
             __syncwarp();
             if (lane == 0) mbar_arrive(slot_free);
           }
         }
         const float s0 = na * n0, s1 = kGlu ? na * n1 : s0;
-        if (kb + 1 < nkb) {
-          na = __ldg(sc.a + static_cast<int64_t>(kb + 1) * p.M);
-          n0 = __ldg(sc.w0 + (kb + 1) * w_step);
-          if constexpr (kGlu) n1 = __ldg(sc.w1 + (kb + 1) * w_step);
-        } else if (t + static_cast<int>(gridDim.x) < total) {
+        if (kb + 1 < p.nkb) {
+          fetch();
+        } else if (t + t_step < total) {
           // the next tile's first scales arrive during this tile's epilogue
-          tl = tile8_at(list, t + gridDim.x, tl.a);
-          sc = scales_of(tl);
-          na = __ldg(sc.a);
-          n0 = __ldg(sc.w0);
-          if constexpr (kGlu) n1 = __ldg(sc.w1);
+          enter(t + t_step);
+          fetch();
         }
         const int b = static_cast<int>(it & 1);
-        const bool r = mbar_wait(acc_full(b), static_cast<uint32_t>((it >> 1) & 1), abort_flag);
+        const bool r = mbar_wait8(acc_full(b), static_cast<uint32_t>((it >> 1) & 1), abort_at);
         if (!__shfl_sync(0xffffffffu, r ? 1 : 0, 0)) { ok = false; break; }
         tc_fence_after();
         const uint32_t tb = tq + static_cast<uint32_t>(b) * 256u;
-        // Four chunks of 32 columns, the next one loaded while this one is added.
-        uint32_t v[2][32];
-        tmem_ld_32x32b_x32(tb + col0, v[0]);
-        tmem_wait_ld();
+        // Two chunks of 32 columns in flight; the next one is requested as soon as
+        // a chunk's registers are free.
+        uint32_t v0[32], v1[32];
+        tmem_ld_32x32b_x32(tb + col0, v0);
+        tmem_ld_32x32b_x32(tb + col0 + 32u, v1);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c < 3) tmem_ld_32x32b_x32(tb + (c < 1 ? col0 + 32u : col1 + 32u * (c - 1)), v[(c + 1) & 1]);
-          const float s = c < 2 ? s0 : s1;
-          const uint64_t ss = pair2(s, s);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) fma2(acc2[16 * c + j], ss, v[c & 1][2 * j], v[c & 1][2 * j + 1]);
-          if (c < 3) tmem_wait_ld();
-          if (c == 2) {               // everything is in registers: the buffer is free
+        for (int h = 0; h < 2; ++h) {
+          tmem_wait_ld();
+          if (h == 1) {                 // everything is in registers: the buffer is free
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(acc_empty(b));
+            if (lane == 0) {
+              if constexpr (PAIR) arrive_remote(cluster_addr(acc_empty(b), 0));
+              else mbar_arrive(acc_empty(b));
+            }
           }
+          const float s = h ? s1 : s0;
+          const uint64_t ss = pair2(s, s);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) fma2(acc2[32 * h + j], ss, v0[2 * j], v0[2 * j + 1]);
+          if (h == 0) tmem_ld_32x32b_x32(tb + col1, v0);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) fma2(acc2[32 * h + 16 + j], ss, v1[2 * j], v1[2 * j + 1]);
+          if (h == 0) tmem_ld_32x32b_x32(tb + col1 + 32u, v1);
         }
       }
       if constexpr (kGluBwd) {
-        if (ok) ok = mbar_wait(gu_bar, static_cast<uint32_t>(li & 1), abort_flag);
+        if (ok) ok = mbar_wait8(gu_bar, li, abort_at);
         ok = __all_sync(0xffffffffu, ok);
       }
       if (!ok) break;
@@ -562,14 +652,14 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
       if constexpr (kGlu) {
         // acc[0..63] gate, acc[64..127] up of features f0 ..; the slot holds
         // [64 B h][64 B gate][64 B up].
-        const int f0 = ft * 128 + wg * 64;
+        const int f0 = cur_ft * 128 + wg * 64;
         if (p.saved != nullptr) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int e = fp8_block_exp(finite_amax<32>(acc + 32 * c));
             quantize32(acc + 32 * c, exp2_int(-e), slot + 64u + 32u * c);
             const int grp = ((c < 2 ? f0 : f_half + f0) >> 5) + (c & 1);
-            if (row_ok) p.saved_scales[static_cast<int64_t>(grp) * p.M + row] = static_cast<uint8_t>(e + 127);
+            if (cur_row >= 0) p.saved_scales[static_cast<int64_t>(grp) * p.M + cur_row] = static_cast<uint8_t>(e + 127);
           }
         }
 #pragma unroll
@@ -578,30 +668,30 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
         // The block of 128 features spans both column halves. Two exchange
         // buffers in turn: passing tile n + 1's barrier means that everybody
         // has read tile n's, which tile n + 2 then writes.
-        float* xch = row_amax + (li & 1) * 2 * kRows8;
+        float* xch = row_amax + li * 2 * kRows8;
         xch[wg * kRows8 + r_in] = m;
         __syncwarp();
         if (lane == 0) mbar_arrive(amax_bar);
-        const bool met = mbar_wait(amax_bar, static_cast<uint32_t>(li & 1), abort_flag);
+        const bool met = mbar_wait8(amax_bar, li, abort_at);
         if (!__shfl_sync(0xffffffffu, met ? 1 : 0, 0)) break;
         m = fmaxf(m, xch[(wg ^ 1) * kRows8 + r_in]);
         const int e = fp8_block_exp(m);
         quantize32(acc, exp2_int(-e), slot);
         quantize32(acc + 32, exp2_int(-e), slot + 32u);
         fence_proxy_async_smem();
-        if (row_ok) {
-          bulk_store(p.out + static_cast<int64_t>(row) * f_half + f0, slot, 64);
+        if (cur_row >= 0) {
+          bulk_store(p.out + static_cast<int64_t>(cur_row) * f_half + f0, slot, 64);
           if (p.saved != nullptr) {
-            uint8_t* sv = p.saved + static_cast<int64_t>(row) * p.N + f0;
+            uint8_t* sv = p.saved + static_cast<int64_t>(cur_row) * p.N + f0;
             bulk_store(sv, slot + 64u, 64);
             bulk_store(sv + f_half, slot + 128u, 64);
           }
-          if (wg == 0) p.out_scales[static_cast<int64_t>(ft) * p.M + row] = exp2_int(e);
+          if (wg == 0) p.out_scales[static_cast<int64_t>(cur_ft) * p.M + cur_row] = exp2_int(e);
         }
       } else if constexpr (kGluBwd) {
         // dh of features f0 .. f0 + 127; the slot holds [128 B g][128 B u][4 + 4
         // scales] and then [128 B dg][128 B du].
-        const int f0 = ft * 256 + wg * 128;
+        const int f0 = cur_ft * 256 + wg * 128;
         const int K = p.K;
         {
           const uint2 gu_scales = lds64(slot + 256u);
@@ -671,26 +761,26 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
             sts128(slot + 128u + 16u * c, ou[0], ou[1], ou[2], ou[3]);
           }
           fence_proxy_async_smem();
-          if (row_ok && f0 < K) {
-          uint8_t* dst = p.out + static_cast<int64_t>(row) * (2 * K) + f0;
+          if (cur_row >= 0 && f0 < K) {
+          uint8_t* dst = p.out + static_cast<int64_t>(cur_row) * (2 * K) + f0;
           bulk_store(dst, slot, 128);
           bulk_store(dst + K, slot + 128u, 128);
           const int64_t blk = f0 / 128;
-          p.out_scales[blk * p.M + row] = exp2_int(eg);
-          p.out_scales[(blk + K / 128) * p.M + row] = exp2_int(eu);
+          p.out_scales[blk * p.M + cur_row] = exp2_int(eg);
+          p.out_scales[(blk + K / 128) * p.M + cur_row] = exp2_int(eu);
           }
         }
       } else {
         const int F = BWD ? p.K : p.N;
-        const int f0 = ft * 256 + wg * 128;
+        const int f0 = cur_ft * 256 + wg * 128;
 #pragma unroll
         for (int c = 0; c < 16; ++c)
           sts128(slot + 16u * c, pack_bf16x2(acc[8 * c], acc[8 * c + 1]),
                  pack_bf16x2(acc[8 * c + 2], acc[8 * c + 3]), pack_bf16x2(acc[8 * c + 4], acc[8 * c + 5]),
                  pack_bf16x2(acc[8 * c + 6], acc[8 * c + 7]));
         fence_proxy_async_smem();
-        if (row_ok && f0 < F)          // F % 16 == 0: whole 32-byte pieces
-          bulk_store(p.out + 2 * (static_cast<int64_t>(row) * F + f0), slot,
+        if (cur_row >= 0 && f0 < F)          // F % 16 == 0: whole 32-byte pieces
+          bulk_store(p.out + 2 * (static_cast<int64_t>(cur_row) * F + f0), slot,
                      2u * static_cast<uint32_t>(min(128, F - f0)));
       }
       bulk_commit();
@@ -699,26 +789,66 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
   }
 
   tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  // A pair frees its tensor memory only when the even CTA's MMAs, which read
+  // and write both CTAs, have drained and both epilogues are done.
+  if constexpr (PAIR) cluster_sync_all(); else __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem_base, 512);
+  if (warp == 1) {
+    if constexpr (PAIR) tmem_dealloc_pair(tmem_base, 512); else tmem_dealloc(tmem_base, 512);
+  }
+}
+
+template <int BWD, int EPI>
+cudaError_t launch_fp8_gemm_t(const CUtensorMap& ta, const CUtensorMap& tw, const Fp8GemmArgs& p,
+                              bool pair, int grid, cudaStream_t s) {
+  auto k = pair ? grouped_fp8_gemm_kernel<BWD, EPI, 1> : grouped_fp8_gemm_kernel<BWD, EPI, 0>;
+  const size_t smem = smem_bytes8(p.E, pair);
+  cudaError_t err =
+      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (err != cudaSuccess) return err;
+  if (!pair) return launch_pdl(k, dim3(grid), dim3(kThreads8), smem, s, ta, tw, p);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads8);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  // Persistent pairs: as many as can be resident together (counted once per device).
+  static std::atomic<int> max_pairs[64];
+  int dev = 0;
+  err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  int n = max_pairs[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cfg.numAttrs = 1;
+    err = cudaOccupancyMaxActiveClusters(&n, k, &cfg);
+    if (err != cudaSuccess) return err;
+    if (n < 1) return cudaErrorInvalidConfiguration;
+    max_pairs[dev].store(n, std::memory_order_relaxed);
+  }
+  cfg.gridDim = dim3(std::min(grid, 2 * n));
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k, ta, tw, p);
 }
 
 }  // namespace
 
 cudaError_t launch_grouped_fp8_gemm(bool bwd, int epi, const CUtensorMap& ta, const CUtensorMap& tw,
-                                    const Fp8GemmArgs& p, int grid, cudaStream_t s) {
-  const size_t smem = smem_bytes8(p.E);
-  auto go = [&](auto kern) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(grid), dim3(kThreads8), smem, s, ta, tw, p);
-  };
-  if (!bwd) return epi == MOE_EPI_SWIGLU ? go(grouped_fp8_gemm_kernel<0, MOE_EPI_SWIGLU>)
-                                         : go(grouped_fp8_gemm_kernel<0, MOE_EPI_NONE>);
-  return epi == MOE_EPI_SWIGLU_BWD ? go(grouped_fp8_gemm_kernel<1, MOE_EPI_SWIGLU_BWD>)
-                                   : go(grouped_fp8_gemm_kernel<1, MOE_EPI_NONE>);
+                                    const Fp8GemmArgs& p, bool pair, int grid, cudaStream_t s) {
+  if (!bwd)
+    return epi == MOE_EPI_SWIGLU ? launch_fp8_gemm_t<0, MOE_EPI_SWIGLU>(ta, tw, p, pair, grid, s)
+                                 : launch_fp8_gemm_t<0, MOE_EPI_NONE>(ta, tw, p, pair, grid, s);
+  return epi == MOE_EPI_SWIGLU_BWD ? launch_fp8_gemm_t<1, MOE_EPI_SWIGLU_BWD>(ta, tw, p, pair, grid, s)
+                                   : launch_fp8_gemm_t<1, MOE_EPI_NONE>(ta, tw, p, pair, grid, s);
 }
 
 }  // namespace moeq

@@ -15,6 +15,7 @@ struct Fp8GemmArgs {
   int32_t M;                   // rows
   int32_t R;                   // reduction length (forward: K; backward: N)
   int32_t n_ftiles;            // feature tiles per expert
+  int32_t nkb, NB, KB;         // 128-wide blocks of R, N and K
   const float* a_scales;       // [ceil(R/128)][M]
   const float* w_scales;       // [E][ceil(N/128)][ceil(K/128)]
   uint8_t* out;                // bf16 [M][F], or e4m3 rows (SwiGLU epilogues)
@@ -23,7 +24,8 @@ struct Fp8GemmArgs {
   uint8_t* saved_scales;       // checkpoint E8M0 [2f/32][M]
 };
 
+// pair: clusters of two CTAs on 256 token rows (grid: CTAs, even).
 cudaError_t launch_grouped_fp8_gemm(bool bwd, int epi, const CUtensorMap& ta, const CUtensorMap& tw,
-                                    const Fp8GemmArgs& p, int grid, cudaStream_t s);
+                                    const Fp8GemmArgs& p, bool pair, int grid, cudaStream_t s);
 
 }  // namespace moeq
