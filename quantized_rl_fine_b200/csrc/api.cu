@@ -517,7 +517,14 @@ moe_status run_fp8_gemm(bool bwd, int epi, const void* rows, const float* row_sc
   const int F = bwd ? w->K : (epi == MOE_EPI_SWIGLU ? w->N / 2 : w->N);
   const int tile_f = (!bwd && epi == MOE_EPI_SWIGLU) ? 128 : 256;
   CUtensorMap ta, tw;
-  bool pair = M > 256 * static_cast<int64_t>(w->E);
+  // CTA pairs (256-row tiles) once the mean expert holds more than 512 rows: a
+  // pair moves a third less weight through L2 and shared memory per product,
+  // but pads an expert's rows to 256 instead of 128, and below about 300 rows
+  // the weight stream is the bound, which single CTAs feed better. Measured
+  // (48 experts, K = 7168, N = 4096; single / pair, us): 100 rows 299 / 410,
+  // 300 rows 787 / 912, 512 rows 990 / 1107, 700 rows 1387 / 1295, 768 rows
+  // 1494 / 1278. MOEQ_F8PAIR=0/1 overrides (tuning).
+  bool pair = M > 512 * static_cast<int64_t>(w->E);
   if (const char* env = getenv("MOEQ_F8PAIR")) pair = atoi(env) == 1;
   // Rows and weights as boxes of 128 bytes x 128 rows, 128-byte swizzle; what
   // lies past the reduction length, the features or the rows reads as zeros.

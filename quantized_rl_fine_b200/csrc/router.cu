@@ -4,6 +4,10 @@
 //
 // The group tables and the row permutation are those of route.cu; only the
 // selection differs. Definitions: include/moeq.h, moe_route_scored.
+//
+// A token's selection is a chain of dependent warp reductions (about 2 us),
+// so what bounds it is latency: a warp per token, everything in registers,
+// three launches for many tokens and one for a decode batch.
 #include <algorithm>
 
 #include "common.cuh"
@@ -13,197 +17,483 @@ namespace moeq {
 
 namespace {
 
-constexpr int kScoredThreads = 512;   // 16 warps, four tokens each in large launches
+// 32 warps: two tokens each in large launches, one in small ones.
+constexpr int kScoredThreads = 1024;
 constexpr int kScoredWarps = kScoredThreads / 32;
-
-// Unsigned integer with the order of the doubles (no NaN; -0 is +0). Real
-// values map to at least 2^52 - 1, which leaves 0 and 1 for the two kinds of
-// entry below every key.
-constexpr unsigned long long kKeyOut = 0ull;      // not a candidate (taken, or of a closed group)
-constexpr unsigned long long kKeyMasked = 1ull;   // a masked expert: chosen last, in ascending id
-__device__ __forceinline__ unsigned long long ordered_key(double v) {
-  const long long b = __double_as_longlong(v + 0.0);
-  return static_cast<unsigned long long>(b) ^
-         (b < 0 ? 0xffffffffffffffffull : 0x8000000000000000ull);
-}
 
 // False for NaN and -inf, which mask an expert.
 __device__ __forceinline__ bool is_open(float l) { return l > -INFINITY; }
 
 __device__ __forceinline__ double sigmoid64(float l) { return 1.0 / (1.0 + exp(-static_cast<double>(l))); }
 
-// One warp per token. Without a bias the logits themselves order the experts;
-// KEYS64: scores are needed in 64 bits, for biased keys or for group sums.
-// Each selection step takes the warp's largest 64-bit key with three integer
-// warp reductions (high word, low word, lowest id), so ties need no shuffles.
-template <int NPER, bool KEYS64>
-__global__ void __launch_bounds__(kScoredThreads)
-route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ bias, int T, int E,
-                    int k, int tpb, moe_router rt, int32_t* __restrict__ topk_idx,
-                    float* __restrict__ gates, int32_t* __restrict__ block_counts) {
-  extern __shared__ double scored_sm[];   // groups > 1: [warps][E] keys; then [E] histogram
-  grid_dependency_wait();
-  grid_dependents_launch();
-  const bool grouped = rt.groups > 1;
-  int32_t* hist = reinterpret_cast<int32_t*>(scored_sm + (grouped ? kScoredWarps * E : 0));
-  const bool with_hist = block_counts != nullptr;
-  if (with_hist)
-    for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
-  __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// Unsigned integers with the order of the floating numbers (no NaN; -0 is +0).
+// Numbers map far above the two values kept for entries below every key.
+constexpr uint32_t kKeyOut = 0u;      // not a candidate (taken, or of a closed group)
+constexpr uint32_t kKeyMasked = 1u;   // a masked expert: chosen last, in ascending id
+__device__ __forceinline__ uint32_t ordered_key(float v) {
+  const int b = __float_as_int(v + 0.0f);
+  return static_cast<uint32_t>(b) ^ (b < 0 ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ unsigned long long ordered_key(double v) {
+  const long long b = __double_as_longlong(v + 0.0);
+  return static_cast<unsigned long long>(b) ^
+         (b < 0 ? 0xffffffffffffffffull : 0x8000000000000000ull);
+}
+
+struct WarpBest {
+  uint32_t hi, lo;   // the key (lo: low word of a 64-bit key, else 0)
+  int idx;
+};
+
+// The warp's largest (key, then lowest id) of one candidate per lane, by
+// integer warp reductions.
+__device__ __forceinline__ WarpBest warp_best(uint32_t key, int idx) {
   const unsigned full = 0xffffffffu;
-  const int per_warp = tpb / kScoredWarps;
-  double* wkeys = scored_sm + static_cast<int64_t>(warp) * E;
+  WarpBest r;
+  r.hi = __reduce_max_sync(full, key);
+  r.lo = 0u;
+  r.idx = static_cast<int>(__reduce_min_sync(full, key == r.hi ? static_cast<uint32_t>(idx) : 0x7fffffffu));
+  return r;
+}
+__device__ __forceinline__ WarpBest warp_best(unsigned long long key, int idx) {
+  const unsigned full = 0xffffffffu;
+  const uint32_t hi = static_cast<uint32_t>(key >> 32), lo = static_cast<uint32_t>(key);
+  WarpBest r;
+  r.hi = __reduce_max_sync(full, hi);
+  r.lo = __reduce_max_sync(full, hi == r.hi ? lo : 0u);
+  r.idx = static_cast<int>(__reduce_min_sync(
+      full, (hi == r.hi && lo == r.lo) ? static_cast<uint32_t>(idx) : 0x7fffffffu));
+  return r;
+}
+
+// Elements from one group's values to the next in the warp's scratch: L lanes
+// read a group, and a distance of L modulo 32 puts the 32 lanes' reads in
+// distinct banks.
+__host__ __device__ constexpr int group_lanes(int groups) {
+  int P = 1;
+  while (P < groups) P <<= 1;
+  return 32 / P;
+}
+__host__ __device__ constexpr int group_pitch(int E, int groups) {
+  const int gsize = E / groups;
+  return gsize + ((group_lanes(groups) - gsize) & 31);
+}
+
+// e / gsize for e < 1024: the high word of e times ceil(2^32 / gsize) (an
+// integer division takes some 20 instructions, and there are two an expert).
+__device__ __forceinline__ uint32_t group_magic(int gsize) { return 0xffffffffu / static_cast<uint32_t>(gsize) + 1u; }
+__device__ __forceinline__ int group_of(int e, uint32_t magic) {
+  return magic == 0u ? e : static_cast<int>(__umulhi(static_cast<uint32_t>(e), magic));   // (0: one expert a group)
+}
+
+// Group scores and the open groups of one token, from the experts' values in
+// gv (lane l: experts l + 32 i; -inf where masked) through the warp's row of
+// shared memory. 32 / P lanes per group (P: groups rounded up to a power of
+// two) each take every (32 / P)-th value and merge their two largest; lane g
+// then holds group g's score, and a group stays open when fewer than
+// topk_groups groups come before it. *gap: the distance between the last open
+// and the first closed group's score.
+template <typename Real, int NPER>
+__device__ __forceinline__ unsigned open_groups(const Real (&gv)[NPER], Real* wrow, int E, const moe_router& rt,
+                                                int lane, uint32_t magic, Real* gap) {
+  const unsigned full = 0xffffffffu;
+  const Real none = static_cast<Real>(-INFINITY);
   const int gsize = E / rt.groups;
-  const bool softmax = rt.score == MOE_SCORE_SOFTMAX;
-  for (int u = 0; u < per_warp; ++u) {
-    const int t = blockIdx.x * tpb + warp * per_warp + u;
-    if (t >= T) break;
-    const float* row = logits + static_cast<int64_t>(t) * E;
-    float l[NPER];
-    float mx = -INFINITY;
+  const int L = group_lanes(rt.groups), pitch = group_pitch(E, rt.groups);
 #pragma unroll
-    for (int i = 0; i < NPER; ++i) {
-      const int e = lane + 32 * i;
-      const float v = (e < E) ? __ldg(row + e) : -INFINITY;
-      l[i] = is_open(v) ? v : -INFINITY;
-      mx = fmaxf(mx, l[i]);
+  for (int i = 0; i < NPER; ++i) {
+    const int e = lane + 32 * i;
+    if (e < E) wrow[e + group_of(e, magic) * (pitch - gsize)] = gv[i];
+  }
+  __syncwarp();
+  const int g = lane / L;
+  Real a = none, b = none;
+  if (g < rt.groups) {
+#pragma unroll 4
+    for (int m = lane % L; m < gsize; m += L) {
+      const Real v = wrow[g * pitch + m];
+      b = fmax(b, fmin(a, v));
+      a = fmax(a, v);
     }
-    double total = 1.0;                  // softmax: sum of exp(l - mx)
-    if (softmax) {
+  }
+  for (int o = 1; o < L; o <<= 1) {
+    const Real oa = __shfl_xor_sync(full, a, o), ob = __shfl_xor_sync(full, b, o);
+    b = fmax(fmin(a, oa), fmax(b, ob));
+    a = fmax(a, oa);
+  }
+  const Real mine = (rt.group_top == 2 && b > none) ? a + b : a;
+  const Real gs = __shfl_sync(full, mine, min(lane, rt.groups - 1) * L);
+  int before = 0;
+  for (int o = 0; o < rt.groups; ++o) {
+    const Real v = __shfl_sync(full, gs, o);
+    before += (v > gs || (v == gs && o < lane)) ? 1 : 0;
+  }
+  const bool open = lane < rt.groups && before < rt.topk_groups;
+  // Smallest open and largest closed score.
+  Real lo_open = open ? gs : static_cast<Real>(INFINITY);
+  Real hi_closed = (lane < rt.groups && !open) ? gs : none;
+  for (int o = 16; o > 0; o >>= 1) {
+    lo_open = fmin(lo_open, __shfl_xor_sync(full, lo_open, o));
+    hi_closed = fmax(hi_closed, __shfl_xor_sync(full, hi_closed, o));
+  }
+  *gap = (rt.topk_groups < rt.groups) ? lo_open - hi_closed : static_cast<Real>(INFINITY);
+  __syncwarp();
+  return __ballot_sync(full, open);
+}
+
+// One token by one warp: lane j < k gets the j-th selected expert in my_idx,
+// and whether it is unmasked in my_open; mx and total are the softmax's
+// maximum and sum.
+//
+// Keys are compared as if in 64 bits. Without a bias the logits have the
+// keys' order and are compared themselves, exactly. With a bias the keys are
+// first formed in FP32, where each is off by less than 2^-18 (1 + |key|): expf 2
+// ulp, a sum of positive numbers at most 37 additions deep, a quotient, one
+// addition. If every two neighbours of the sorted selection, the first one
+// left out, and the groups around the cut lie further apart than twice that,
+// the selection is the one in 64 bits. Where only neighbours are too close
+// (about one token in 100 for normal logits), the experts that may belong to
+// the selection, at most 32, are ordered by their keys in 64 bits, one a lane;
+// otherwise (groups too close, more than 32 equal keys, masked experts
+// reached) the whole token is done again in 64 bits.
+template <int NPER>
+__device__ __forceinline__ void select_token(const float* __restrict__ row, const float* __restrict__ bias, int E,
+                                             int k, const moe_router& rt, double* wrow, int lane, float* mx_out,
+                                             double* total_out, int* my_idx_out, bool* my_open_out) {
+  const unsigned full = 0xffffffffu;
+  const bool grouped = rt.groups > 1, softmax = rt.score == MOE_SCORE_SOFTMAX;
+  const uint32_t magic = group_magic(E / rt.groups);
+  float l[NPER], ez[NPER];              // logits (masked: -inf); softmax: exp(l - mx)
+  float mx = -INFINITY;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(full, mx, o));
-      if constexpr (KEYS64) {
-        double z = 0.0;
+  for (int i = 0; i < NPER; ++i) {
+    const int e = lane + 32 * i;
+    const float v = (e < E) ? __ldg(row + e) : -INFINITY;
+    l[i] = is_open(v) ? v : -INFINITY;
+    ez[i] = 0.0f;
+    mx = fmaxf(mx, l[i]);
+  }
+  float z = 1.0f;
+  if (softmax) {
 #pragma unroll
-        for (int i = 0; i < NPER; ++i)
-          if (is_open(l[i])) z += (l[i] == mx) ? 1.0 : exp(static_cast<double>(l[i]) - mx);
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(full, mx, o));
+    z = 0.0f;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(full, z, o);
-        total = z;
-      } else {
-        float z = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NPER; ++i)
-          if (is_open(l[i])) z += (l[i] == mx) ? 1.0f : expf(l[i] - mx);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(full, z, o);
-        total = z;
-      }
-    }
-    // Score of an expert with an unmasked logit (+inf included).
-    auto score64 = [&](float v) {
-      if (softmax) return ((v == mx) ? 1.0 : exp(static_cast<double>(v) - mx)) / total;
-      return sigmoid64(v);
-    };
-    unsigned long long key[NPER];
-#pragma unroll
-    for (int i = 0; i < NPER; ++i) {
-      const int e = lane + 32 * i;
-      key[i] = kKeyOut;
-      if (e >= E) continue;
-      // kv orders the experts, gv is what groups add up.
-      double kv = -INFINITY, gv = -INFINITY;
+    for (int i = 0; i < NPER; ++i)
       if (is_open(l[i])) {
-        kv = gv = static_cast<double>(l[i]);
-        if constexpr (KEYS64) {
-          gv = score64(l[i]);
-          if (bias) {
-            gv += static_cast<double>(__ldg(bias + e));
-            kv = gv = (gv > -INFINITY) ? gv : -INFINITY;
-          }
-        }
+        ez[i] = (l[i] == mx) ? 1.0f : expf(l[i] - mx);
+        z += ez[i];
       }
-      key[i] = (kv > -INFINITY) ? ordered_key(kv) : kKeyMasked;
-      if (grouped) wkeys[e] = gv;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(full, z, o);
+  }
+  const float zinv = 1.0f / z;
+  *mx_out = mx;
+  *total_out = z;
+  const bool scores = bias != nullptr || (grouped && rt.group_top == 2);   // else logits do for all
+  int my_idx = 0;
+  bool my_open = false, sure = true;
+  {
+    uint32_t key[NPER];
+    float gv[NPER];
+    float top = 0.0f;                     // largest magnitude of a key, for its error
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) {
+      const int e = lane + 32 * i;
+      float kv = l[i];
+      gv[i] = l[i];
+      if (scores && is_open(l[i])) {
+        gv[i] = softmax ? ez[i] * zinv : __fdividef(1.0f, 1.0f + __expf(-l[i]));
+        if (bias) {
+          gv[i] += __ldg(bias + e);
+          if (!(gv[i] > -INFINITY)) gv[i] = -INFINITY;
+          kv = gv[i];
+        }
+        if (gv[i] > -INFINITY) top = fmaxf(top, fabsf(gv[i]));
+      }
+      key[i] = (e < E) ? ((kv > -INFINITY) ? ordered_key(kv) : kKeyMasked) : kKeyOut;
+    }
+    float err = 0.0f;
+    if (scores) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(full, top, o));
+      err = 3.814697265625e-6f * (1.0f + top);   // 2^-18
     }
     if (grouped) {
-      // 32 / P lanes per group (P: groups rounded up to a power of two) each
-      // take every (32 / P)-th key of the group and merge their two largest.
-      __syncwarp();
-      int P = 1;
-      while (P < rt.groups) P <<= 1;
-      const int L = 32 / P;
-      const int g = lane / L, sub = lane % L;
-      double a = -INFINITY, b = -INFINITY;
-      if (g < rt.groups) {
-        for (int m = sub; m < gsize; m += L) {
-          const double v = wkeys[g * gsize + m];
-          if (v > a) { b = a; a = v; } else if (v > b) { b = v; }
-        }
-      }
-      for (int o = 1; o < L; o <<= 1) {
-        const double oa = __shfl_xor_sync(full, a, o), ob = __shfl_xor_sync(full, b, o);
-        b = fmax(fmin(a, oa), fmax(b, ob));
-        a = fmax(a, oa);
-      }
-      const double mine = (rt.group_top == 2 && b > -INFINITY) ? a + b : a;
-      // Lane g holds group g; a group stays open when fewer than topk_groups
-      // groups come before it.
-      const double gs = __shfl_sync(full, mine, min(lane, rt.groups - 1) * L);
-      int before = 0;
-      for (int o = 0; o < rt.groups; ++o) {
-        const double v = __shfl_sync(full, gs, o);
-        before += (v > gs || (v == gs && o < lane)) ? 1 : 0;
-      }
-      const unsigned open = __ballot_sync(full, lane < rt.groups && before < rt.topk_groups);
+      float gap;
+      const unsigned open = open_groups<float, NPER>(gv, reinterpret_cast<float*>(wrow), E, rt, lane, magic, &gap);
+      // a group score is one value or the sum of two
+      if (scores) sure = gap > 2.0f * rt.group_top * err;
 #pragma unroll
       for (int i = 0; i < NPER; ++i) {
         const int e = lane + 32 * i;
-        if (e < E && !((open >> (e / gsize)) & 1u)) key[i] = kKeyOut;
+        if (e < E && !((open >> group_of(e, magic)) & 1u)) key[i] = kKeyOut;
       }
-      __syncwarp();
     }
-    // k rounds of the warp's best key.
-    unsigned long long bk = kKeyOut;
-    int bi = 0x7fffffff;
-    auto local_best = [&]() {
-      bk = kKeyOut;
-      bi = 0x7fffffff;
+    // k rounds; with inexact keys more, while a key may still belong to the
+    // selection (it is within reach of the k-th), and one for the first that
+    // cannot. Lane j holds the j-th candidate.
+    // Each lane keeps its three best keys in order; a lane that has given all
+    // three (rare: four of the selected experts in one lane) looks through its
+    // keys again for those behind the last one it gave.
+    uint32_t q0, q1, q2;
+    int i0, i1, i2;
+    auto refill = [&](uint32_t below, int after) {
+      q0 = q1 = q2 = kKeyOut;
+      i0 = i1 = i2 = 0x7fffffff;
+#pragma unroll
+      for (int i = 0; i < NPER; ++i) {
+        const int e = lane + 32 * i;
+        const uint32_t kx = (key[i] < below || (key[i] == below && e > after)) ? key[i] : kKeyOut;
+        // (an equal key stays behind: ascending id)
+        const bool u0 = kx > q0, u1 = kx > q1, u2 = kx > q2;
+        q2 = u1 ? q1 : (u2 ? kx : q2);
+        i2 = u1 ? i1 : (u2 ? e : i2);
+        q1 = u0 ? q0 : (u1 ? kx : q1);
+        i1 = u0 ? i0 : (u1 ? e : i1);
+        q0 = u0 ? kx : q0;
+        i0 = u0 ? e : i0;
+      }
+    };
+    refill(0xffffffffu, 0x7fffffff);
+    int given = 0;
+    const int rounds = bias ? min(32, E) : k;
+    float last = 0.0f, reach = 0.0f;
+    int count = 0;
+    bool close = false, odd = false;      // neighbours too close; only 64 bits will do
+    for (int j = 0; j < rounds; ++j) {
+      const WarpBest best = warp_best(q0, i0);
+      if (bias) {
+        const float v = __uint_as_float(best.hi ^ ((best.hi & 0x80000000u) ? 0x80000000u : 0xffffffffu));
+        const bool real = best.hi > kKeyMasked;
+        if (j >= k && !(real && v >= reach)) break;          // nothing more in reach
+        odd |= !real;
+        close |= j > 0 && !(last - v > 2.0f * err);
+        last = v;
+        if (j == k - 1) reach = v - 4.0f * err;
+      }
+      if (lane == j) {
+        my_idx = best.idx;
+        my_open = best.hi > kKeyMasked;
+      }
+      ++count;
+      const bool gave = i0 == best.idx;
+      if (gave) {
+        q0 = q1;
+        i0 = i1;
+        q1 = q2;
+        i1 = i2;
+        q2 = kKeyOut;
+        i2 = 0x7fffffff;
+        ++given;
+      }
+      if (NPER > 3 && __any_sync(full, gave && given == 3)) {
+        if (gave && given == 3) {
+          refill(best.hi, best.idx);
+          given = 0;
+        }
+      }
+    }
+    if (bias && (close || odd)) {
+      if (odd || count == 32) {
+        sure = false;
+      } else if (sure) {
+        // Order the candidates by their keys in 64 bits.
+        double z64 = 1.0;
+        if (softmax) {
+          z64 = 0.0;
+#pragma unroll
+          for (int i = 0; i < NPER; ++i)
+            if (is_open(l[i])) z64 += (l[i] == mx) ? 1.0 : exp(static_cast<double>(l[i]) - mx);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) z64 += __shfl_xor_sync(full, z64, o);
+        }
+        unsigned long long mine = kKeyOut;
+        if (lane < count) {
+          const float v = __ldg(row + my_idx);
+          const double sv = softmax ? ((v == mx) ? 1.0 : exp(static_cast<double>(v) - mx)) / z64 : sigmoid64(v);
+          mine = ordered_key(sv + static_cast<double>(__ldg(bias + my_idx)));
+        }
+        const int cand = my_idx;
+        for (int j = 0; j < k; ++j) {
+          const WarpBest best = warp_best(mine, lane < count ? cand : 0x7fffffff);
+          if (lane == j) my_idx = best.idx;
+          if (lane < count && cand == best.idx) mine = kKeyOut;
+        }
+        my_open = lane < k;
+      }
+    }
+  }
+  if (scores && !__all_sync(full, sure)) {
+    // In 64 bits.
+    double z64 = 1.0;
+    if (softmax) {
+      z64 = 0.0;
+#pragma unroll
+      for (int i = 0; i < NPER; ++i)
+        if (is_open(l[i])) z64 += (l[i] == mx) ? 1.0 : exp(static_cast<double>(l[i]) - mx);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) z64 += __shfl_xor_sync(full, z64, o);
+      *total_out = z64;
+    }
+    unsigned long long key[NPER];
+    double gv[NPER];
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) {
+      const int e = lane + 32 * i;
+      double kv = l[i];
+      gv[i] = l[i];
+      if (is_open(l[i])) {
+        gv[i] = softmax ? ((l[i] == mx) ? 1.0 : exp(static_cast<double>(l[i]) - mx)) / z64 : sigmoid64(l[i]);
+        if (bias) {
+          gv[i] += static_cast<double>(__ldg(bias + e));
+          if (!(gv[i] > -INFINITY)) gv[i] = -INFINITY;
+          kv = gv[i];
+        }
+      }
+      key[i] = (e < E) ? ((kv > -INFINITY) ? ordered_key(kv) : kKeyMasked) : kKeyOut;
+    }
+    if (grouped) {
+      double gap;
+      const unsigned open = open_groups<double, NPER>(gv, wrow, E, rt, lane, magic, &gap);
+#pragma unroll
+      for (int i = 0; i < NPER; ++i) {
+        const int e = lane + 32 * i;
+        if (e < E && !((open >> group_of(e, magic)) & 1u)) key[i] = kKeyOut;
+      }
+    }
+    for (int j = 0; j < k; ++j) {
+      unsigned long long bk = kKeyOut;
+      int bi = 0x7fffffff;
 #pragma unroll
       for (int i = 0; i < NPER; ++i)
         if (key[i] > bk) {
           bk = key[i];
           bi = lane + 32 * i;
         }
-    };
-    local_best();
-    int my_idx = 0;
-    bool my_open = false;
-    for (int j = 0; j < k; ++j) {
-      const unsigned hi = static_cast<unsigned>(bk >> 32), lo = static_cast<unsigned>(bk);
-      const unsigned mh = __reduce_max_sync(full, hi);
-      const unsigned ml = __reduce_max_sync(full, hi == mh ? lo : 0u);
-      const int best = static_cast<int>(
-          __reduce_min_sync(full, (hi == mh && lo == ml) ? static_cast<unsigned>(bi) : 0x7fffffffu));
+      const WarpBest best = warp_best(bk, bi);
       if (lane == j) {
-        my_idx = best;
-        my_open = mh != 0u;
+        my_idx = best.idx;
+        my_open = best.hi != 0u;
       }
-      if ((best & 31) == lane) {
 #pragma unroll
-        for (int i = 0; i < NPER; ++i)
-          if (i == (best >> 5)) key[i] = kKeyOut;
-        local_best();
-      }
+      for (int i = 0; i < NPER; ++i)
+        if (lane + 32 * i == best.idx) key[i] = kKeyOut;
     }
-    // The k selected scores in 64 bits: with renorm even scores that FP32
-    // cannot hold (a sigmoid far below zero) give their gates.
-    const double s = (lane < k && my_open) ? score64(__ldg(row + my_idx)) : 0.0;
-    double sum = s;
+  }
+  *my_idx_out = my_idx;
+  *my_open_out = my_open && lane < k;
+}
+
+// Gate of the lane's selected expert, in FP32; where renorm divides by a sum
+// that FP32 hardly holds (sigmoids far below zero), in 64 bits.
+__device__ __forceinline__ float gate_of(const float* __restrict__ row, int idx, bool open, float mx, double total,
+                                         const moe_router& rt) {
+  const unsigned full = 0xffffffffu;
+  const bool softmax = rt.score == MOE_SCORE_SOFTMAX;
+  float s = 0.0f, v = 0.0f;
+  if (open) {
+    v = __ldg(row + idx);
+    s = softmax ? ((v == mx) ? 1.0f : expf(v - mx)) / static_cast<float>(total) : 1.0f / (1.0f + expf(-v));
+  }
+  if (!rt.renorm) return rt.scale * s;
+  float sum = s;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(full, sum, o);
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(full, sum, o);
+  if (sum > 1e-30f) return rt.scale * (s / sum);
+  double s64 = 0.0;
+  if (open) s64 = softmax ? ((v == mx) ? 1.0 : exp(static_cast<double>(v) - mx)) / total : sigmoid64(v);
+  double sum64 = s64;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum64 += __shfl_xor_sync(full, sum64, o);
+  return static_cast<float>(rt.scale * (sum64 > 0.0 ? s64 / sum64 : 0.0));
+}
+
+// tpb tokens per block; block_counts == nullptr skips the per-block histogram.
+template <int NPER>
+__global__ void __launch_bounds__(kScoredThreads, 1)
+route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ bias, int T, int E, int k, int tpb,
+                    int row_el, moe_router rt, int32_t* __restrict__ topk_idx, float* __restrict__ gates,
+                    int32_t* __restrict__ block_counts) {
+  extern __shared__ double scored_sm[];   // [warps][row_el] group scratch; then [E] histogram
+  grid_dependency_wait();
+  grid_dependents_launch();
+  int32_t* hist = reinterpret_cast<int32_t*>(scored_sm + min(tpb, kScoredWarps) * row_el);
+  const bool with_hist = block_counts != nullptr;
+  if (with_hist)
+    for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int u = warp; u < tpb; u += kScoredWarps) {
+    const int t = blockIdx.x * tpb + u;
+    if (t >= T) break;
+    const float* row = logits + static_cast<int64_t>(t) * E;
+    float mx;
+    double total;
+    int idx;
+    bool open;
+    select_token<NPER>(row, bias, E, k, rt, scored_sm + warp * row_el, lane, &mx, &total, &idx,
+                       &open);
+    const float w = gate_of(row, idx, open, mx, total, rt);
     if (lane < k) {
-      const double w = rt.renorm ? (sum > 0.0 ? s / sum : 0.0) : s;
-      topk_idx[static_cast<int64_t>(t) * k + lane] = my_idx;
-      gates[static_cast<int64_t>(t) * k + lane] = static_cast<float>(rt.scale * w);
-      if (with_hist) atomicAdd(&hist[my_idx], 1);
+      topk_idx[static_cast<int64_t>(t) * k + lane] = idx;
+      gates[static_cast<int64_t>(t) * k + lane] = w;
+      if (with_hist) atomicAdd(&hist[idx], 1);
     }
   }
   if (!with_hist) return;
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += blockDim.x)
     block_counts[static_cast<int64_t>(blockIdx.x) * E + e] = hist[e];
+}
+
+// Up to 32 tokens (a decode batch) in one block and one launch: a warp per
+// token selects, then the block forms the group tables and the permutation
+// from one 32-bit token mask per expert.
+constexpr int kSmallTokens = 32;
+template <int NPER>
+__global__ void __launch_bounds__(kScoredThreads, 1)
+route_scored_small_kernel(const float* __restrict__ logits, const float* __restrict__ bias, int T, int E, int k,
+                          int row_el, moe_router rt, int chunk_size, int32_t* __restrict__ topk_idx, float* __restrict__ gates,
+                          int32_t* __restrict__ offsets, int32_t* __restrict__ active,
+                          int32_t* __restrict__ num_active, int32_t* __restrict__ chunk_offsets,
+                          int32_t* __restrict__ num_chunks, int32_t* __restrict__ perm_token,
+                          int32_t* __restrict__ inv_perm) {
+  extern __shared__ double scored_sm[];   // [T][row_el] group scratch
+  __shared__ uint32_t mask[1024];
+  __shared__ int32_t first[1024];
+  __shared__ int32_t chosen[kSmallTokens * 32];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  mask[tid] = 0u;
+  __syncthreads();
+  if (warp < T) {
+    const float* row = logits + static_cast<int64_t>(warp) * E;
+    float mx;
+    double total;
+    int idx;
+    bool open;
+    select_token<NPER>(row, bias, E, k, rt, scored_sm + warp * row_el, lane, &mx, &total, &idx,
+                       &open);
+    if (lane < k) {
+      chosen[warp * k + lane] = idx;
+      atomicOr(&mask[idx], 1u << warp);
+      topk_idx[warp * k + lane] = idx;
+    }
+    const float w = gate_of(row, idx, open, mx, total, rt);
+    if (lane < k) gates[warp * k + lane] = w;
+  }
+  __syncthreads();
+  first[tid] = scan_experts(tid < E ? __popc(mask[tid]) : 0, E, chunk_size, offsets, active, num_active,
+                            chunk_offsets, num_chunks);
+  __syncthreads();
+  if (tid < T * k) {
+    const int t = tid / k, e = chosen[tid];
+    const int p = first[e] + __popc(mask[e] & ((1u << t) - 1u));
+    perm_token[p] = t;
+    inv_perm[tid] = p;
+  }
 }
 
 // One warp per token: the k selected experts' ds in the lanes, spread into a
@@ -295,36 +585,46 @@ cudaError_t launch_route_scored(const float* logits, const float* bias, const vo
                                 int32_t* num_active, int32_t* chunk_offsets, int32_t* num_chunks,
                                 int32_t* perm_token, int32_t* inv_perm, void* x_perm,
                                 int32_t* block_counts, cudaStream_t s) {
+  const int nper = (E + 31) / 32;
+  // Selects the instantiation and raises its shared-memory limit, past 48 KiB
+  // (more than 192 experts in groups).
+#define MOEQ_BY_NPER(CALL_)             \
+  (nper <= 2 ? CALL_(2)                 \
+   : nper <= 4 ? CALL_(4)               \
+   : nper <= 8 ? CALL_(8)               \
+   : nper <= 12 ? CALL_(12)             \
+   : nper <= 16 ? CALL_(16) : CALL_(32))
+  auto go = [&](auto kern, int blocks, size_t sm, auto... args) {
+    if (sm > 40 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(sm));
+      if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(kern, dim3(blocks), dim3(kScoredThreads), sm, s, args...);
+  };
+  // one warp's group scratch, in doubles
+  const int row_el = rt.groups > 1 ? group_pitch(E, rt.groups) * rt.groups : 0;
+  const size_t row_sm = sizeof(double) * row_el;
+  // Few tokens: tokens of a block so that the scratch fits 200 KiB.
+  const int fit = row_sm == 0 ? kScoredWarps : static_cast<int>(std::min<size_t>(kScoredWarps, (200 * 1024) / row_sm));
+  if (T <= std::min(kSmallTokens, fit) && x == nullptr) {
+#define MOEQ_SMALL(N_)                                                                                             \
+  go(route_scored_small_kernel<N_>, 1, row_sm* T, logits, bias, T, E, k, row_el, rt, chunk_size, topk_idx, gates, \
+     offsets, active, num_active, chunk_offsets, num_chunks, perm_token, inv_perm)
+    return MOEQ_BY_NPER(MOEQ_SMALL);
+#undef MOEQ_SMALL
+  }
   const bool small = route_single_pass(T, E);
   if (!small && block_counts == nullptr) return cudaErrorInvalidValue;
-  const int tpb = small ? kScoredWarps : route_tokens_per_block();
+  const int tpb = small ? fit : route_tokens_per_block();
   const int nblk = (T + tpb - 1) / tpb;
   int32_t* hist_out = small ? nullptr : block_counts;
-  const size_t sm = (rt.groups > 1 ? sizeof(double) * kScoredWarps * E : 0) +
-                    (small ? 0 : sizeof(int32_t) * E);
-  const bool keys64 = bias != nullptr || (rt.groups > 1 && rt.group_top == 2);
-  const int nper = (E + 31) / 32;
-  cudaError_t err;
-  // The shared-memory limit only matters past 48 KiB (more than 384 experts in groups).
-#define MOEQ_SCORED_T(N_, K_)                                                                       \
-  [&]() {                                                                                           \
-    if (sm > 48 * 1024) {                                                                           \
-      const cudaError_t e_ = cudaFuncSetAttribute(                                                  \
-          route_scored_kernel<N_, K_>, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);    \
-      if (e_ != cudaSuccess) return e_;                                                             \
-    }                                                                                               \
-    return launch_pdl(route_scored_kernel<N_, K_>, dim3(nblk), dim3(kScoredThreads), sm, s, logits, \
-                      bias, T, E, k, tpb, rt, topk_idx, gates, hist_out);                           \
-  }()
-#define MOEQ_SCORED(N_) (keys64 ? MOEQ_SCORED_T(N_, true) : MOEQ_SCORED_T(N_, false))
-  if (nper <= 2) err = MOEQ_SCORED(2);
-  else if (nper <= 4) err = MOEQ_SCORED(4);
-  else if (nper <= 8) err = MOEQ_SCORED(8);
-  else if (nper <= 12) err = MOEQ_SCORED(12);
-  else if (nper <= 16) err = MOEQ_SCORED(16);
-  else err = MOEQ_SCORED(32);
-#undef MOEQ_SCORED
-#undef MOEQ_SCORED_T
+  const size_t sm = row_sm * std::min(tpb, kScoredWarps) + (small ? 0 : sizeof(int32_t) * E);
+#define MOEQ_LARGE(N_) \
+  go(route_scored_kernel<N_>, nblk, sm, logits, bias, T, E, k, tpb, row_el, rt, topk_idx, gates, hist_out)
+  const cudaError_t err = MOEQ_BY_NPER(MOEQ_LARGE);
+#undef MOEQ_LARGE
+#undef MOEQ_BY_NPER
   if (err != cudaSuccess) return err;
   return launch_route_tables(x, T, E, k, d, chunk_size, topk_idx, offsets, active, num_active,
                              chunk_offsets, num_chunks, perm_token, inv_perm, x_perm, block_counts,

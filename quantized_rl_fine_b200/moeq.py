@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -345,16 +346,28 @@ def moe_ep_regroup(counts: torch.Tensor, rows: torch.Tensor, direction: int, chu
 # --------------------------------------------------------------------------
 
 def _need(t, name: str, dtype, shape, device=None):
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.shape == shape
+            and t.is_contiguous() and (device is None or t.device == device)):
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name}: libmoeq takes CUDA tensors only")
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    raise ValueError(f"{name}: on {t.device}, expected {device}")
+
+
+# The raw handle of a device's current stream; building a Stream object for it costs 4 us a call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _here(device) -> int:
+    """The current stream of the tensors' device (which is the current one inside _on)."""
+    return _raw_stream(device.index)
 
 
 @contextlib.contextmanager
@@ -384,6 +397,7 @@ class RouterSpec:
     renorm: bool = True           # gates divided by the sum of the selected scores
     scale: float = 1.0            # factor of every gate
 
+    @functools.lru_cache(maxsize=256)
     def c(self) -> RouterC:
         if self.score not in SCORE:
             raise ValueError(f"score {self.score!r}: expected one of {sorted(SCORE)}")
@@ -391,19 +405,36 @@ class RouterSpec:
                        1 if self.renorm else 0, self.scale)
 
 
+@functools.lru_cache(maxsize=256)
+def _scored_ws_bytes(T: int, E: int, k: int, router: RouterSpec, chunk_size: int) -> int:
+    """Workspace of moe_route_scored (a function of the sizes alone)."""
+    wsb = ctypes.c_size_t(0)
+    _check(lib().moe_route_scored(None, None, None, T, E, k, 0, ctypes.byref(router.c()), chunk_size, None,
+                                  None, None, None, None, None, None, None, None, None, None,
+                                  ctypes.byref(wsb), None), "moe_route_scored (workspace query)")
+    return wsb.value
+
+
+@functools.lru_cache(maxsize=256)
+def _routing_sizes(T: int, E: int, k: int) -> tuple[list[int], list[int]]:
+    """Split sizes of one int32 buffer into the eight tables (each starting on 16 bytes) and the
+    padding between them, and which of the pieces are tables."""
+    sizes, tables = [], []
+    for n in (T * k, E + 1, E, 1, E + 1, 1, T * k, T * k):
+        tables.append(len(sizes))
+        sizes.append(n)
+        if n % 4:
+            sizes.append(-n % 4)
+    return sizes, tables
+
+
 def _new_routing(T: int, E: int, k: int, d: int | None, dev) -> Routing:
-    # one allocation for the eight int32 tables, each starting on 16 bytes
-    sizes = (T * k, E + 1, E, 1, E + 1, 1, T * k, T * k)
-    flat = torch.empty(sum(-(-n // 4) * 4 for n in sizes), dtype=torch.int32, device=dev)
-    parts, at = [], 0
-    for n in sizes:
-        parts.append(flat[at:at + n])
-        at += -(-n // 4) * 4
-    return Routing(topk_idx=parts[0].view(T, k),
-                   gates=torch.empty((T, k), dtype=torch.float32, device=dev),
-                   expert_offsets=parts[1], active=parts[2], num_active=parts[3],
-                   chunk_offsets=parts[4], num_chunks=parts[5], perm_token=parts[6],
-                   inv_perm=parts[7],
+    sizes, tables = _routing_sizes(T, E, k)
+    pieces = torch.empty(sum(sizes), dtype=torch.int32, device=dev).split_with_sizes(sizes)
+    idx, off, act, nact, chunk, nchunk, perm, inv = (pieces[i] for i in tables)
+    return Routing(topk_idx=idx.view(T, k), gates=torch.empty((T, k), dtype=torch.float32, device=dev),
+                   expert_offsets=off, active=act, num_active=nact, chunk_offsets=chunk,
+                   num_chunks=nchunk, perm_token=perm, inv_perm=inv,
                    x_perm=None if d is None else torch.empty((T * k, d), dtype=torch.bfloat16, device=dev),
                    E=E, k=k)
 
@@ -436,25 +467,18 @@ def moe_route_scored(logits: torch.Tensor, x: torch.Tensor | None, k: int, chunk
     if x is not None:
         d = x.shape[-1]
         _need(x, "x", torch.bfloat16, (T, d), dev)
-    rc = router.c()
     with _on(dev, stream):
-        L = lib()
-        st = _stream()
-        wsb = ctypes.c_size_t(0)
-        _check(L.moe_route_scored(None, None, None, T, E, k, d or 0, ctypes.byref(rc), chunk_size, None,
-                                  None, None, None, None, None, None, None, None, None, None,
-                                  ctypes.byref(wsb), st), "moe_route_scored (workspace query)")
+        need = _scored_ws_bytes(T, E, k, router, chunk_size)
         if out is None:
             out = _new_routing(T, E, k, d, dev)
         else:
             _need_routing(out, T, E, k, d, dev)
-        ws, wsp, wsz = _workspace(wsb.value, dev)
-        _check(L.moe_route_scored(_p(logits), _p(bias), _p(x), T, E, k, d or 0, ctypes.byref(rc),
-                                  chunk_size, _p(out.topk_idx), _p(out.gates), _p(out.expert_offsets),
-                                  _p(out.active), _p(out.num_active), _p(out.chunk_offsets),
-                                  _p(out.num_chunks), _p(out.perm_token), _p(out.inv_perm),
-                                  _p(out.x_perm) if x is not None else None, wsp, wsz, st),
-               "moe_route_scored")
+        ws, wsp, wsz = _workspace(need, dev)
+        _check(lib().moe_route_scored(
+            _p(logits), _p(bias), _p(x), T, E, k, d or 0, ctypes.byref(router.c()), chunk_size,
+            _p(out.topk_idx), _p(out.gates), _p(out.expert_offsets), _p(out.active), _p(out.num_active),
+            _p(out.chunk_offsets), _p(out.num_chunks), _p(out.perm_token), _p(out.inv_perm),
+            _p(out.x_perm) if x is not None else None, wsp, wsz, _here(dev)), "moe_route_scored")
     return out
 
 
@@ -475,7 +499,7 @@ def moe_route_scored_bwd(d_gates: torch.Tensor, logits: torch.Tensor, routing: R
         else:
             _need(out, "out", torch.float32, (T, E), dev)
         _check(lib().moe_route_scored_bwd(_p(d_gates), _p(logits), _p(routing.topk_idx), T, E, k,
-                                          ctypes.byref(rc), _p(out), _stream()), "moe_route_scored_bwd")
+                                          ctypes.byref(rc), _p(out), _here(dev)), "moe_route_scored_bwd")
     return out
 
 
@@ -498,7 +522,7 @@ def moe_combine_bwd(dy: torch.Tensor, rows: torch.Tensor, routing: Routing, stre
             _need(out, "out", torch.bfloat16, (T * k, D), dev)
         d_gates = torch.empty((T, k), dtype=torch.float32, device=dev)
         _check(lib().moe_combine_bwd(_p(dy), _p(rows), _p(routing.inv_perm), _p(routing.gates), T, k, D,
-                                     _p(out), _p(d_gates), _stream()), "moe_combine_bwd")
+                                     _p(out), _p(d_gates), _here(dev)), "moe_combine_bwd")
     return out, d_gates
 
 
@@ -588,7 +612,7 @@ def moe_quantize_fp8_rows(x: torch.Tensor, routing: Routing | None = None, strea
         else:
             _need_fp8_rows(out, "out", T * k, K, dev)
         _check(lib().moe_quantize_fp8_rows(_p(x), T, K, None if routing is None else _p(routing.inv_perm),
-                                           k, _p(out.q), _p(out.scales), _stream()),
+                                           k, _p(out.q), _p(out.scales), _here(dev)),
                "moe_quantize_fp8_rows")
     return out
 
@@ -606,7 +630,7 @@ def moe_dequantize_fp8_rows(rows: Fp8Rows, stream=None, out: torch.Tensor | None
         else:
             _need(out, "out", torch.bfloat16, (M, K), dev)
         _check(lib().moe_dequantize_fp8_rows(_p(rows.q), _p(rows.scales), M, K, rows.fmt, _p(out),
-                                             _stream()), "moe_dequantize_fp8_rows")
+                                             _here(dev)), "moe_dequantize_fp8_rows")
     return out
 
 
@@ -631,7 +655,7 @@ def moe_grouped_fp8_gemm_fwd(a: Fp8Rows, w: Fp8WeightT, routing: Routing, epi: i
             out = torch.empty((M, w.N), dtype=torch.bfloat16, device=dev)
             outs = (_p(out), None, None, None)
         _check(lib().moe_grouped_fp8_gemm_fwd(_p(a.q), _p(a.scales), M, ctypes.byref(wc), ctypes.byref(g),
-                                              epi, *outs, _stream()), "moe_grouped_fp8_gemm_fwd")
+                                              epi, *outs, _here(dev)), "moe_grouped_fp8_gemm_fwd")
     return (h, saved) if epi == EPI_SWIGLU else out
 
 
@@ -657,7 +681,7 @@ def moe_grouped_fp8_gemm_bwd_dx(dout: Fp8Rows, w: Fp8WeightT, routing: Routing, 
             out = torch.empty((M, w.K), dtype=torch.bfloat16, device=dev)
             outs = (None, None, _p(out), None)
         _check(lib().moe_grouped_fp8_gemm_bwd_dx(_p(dout.q), _p(dout.scales), M, ctypes.byref(wc),
-                                                 ctypes.byref(g), epi, *outs, _stream()),
+                                                 ctypes.byref(g), epi, *outs, _here(dev)),
                "moe_grouped_fp8_gemm_bwd_dx")
     return out
 
