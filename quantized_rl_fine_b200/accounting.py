@@ -18,6 +18,17 @@ def bytes_per_param(fmt: str) -> float:
     return 0.5 + SCALE_BYTES[fmt] / GROUP
 
 
+def fp8_bytes_per_param() -> float:
+    """e4m3 with one fp32 scale per 128 x 128 block."""
+    return 1.0 + 4.0 / (128 * 128)
+
+
+def saved_gu_bytes_per_row(f: int, checkpoint8: bool) -> int:
+    """What a training step keeps of gate|up (2f values) for each row: BF16, or e4m3 with an
+    E8M0 scale per 32 values."""
+    return 2 * f + 2 * f // GROUP if checkpoint8 else 4 * f
+
+
 def storage_estimate(total_params: float, bits: int = 4, group_size: int = 32,
                      scale_bits: int = 8, sensitive_ratio: float = 0.02) -> float:
     """Bytes of a group-quantized checkpoint: quantized body + one scale per

@@ -893,11 +893,12 @@ moe_status moe_combine_bwd(const void* dy, const void* rows, const int32_t* inv_
   MOEQ_TRACE("moe_combine_bwd");
   if (!dy || !rows || !inv_perm || !d_rows || !d_gates) return MOE_ERR_INVALID_ARG;
   if (T < 1 || k < 1 || k > 32 || D < 8 || D % 8 != 0) return MOE_ERR_INVALID_ARG;
-  if (T >= (int64_t(1) << 31) || T * k >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (T >= (int64_t(1) << 31) || T * k >= (int64_t(1) << 31) || D >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
   if (!aligned16(dy) || !aligned16(rows) || !aligned16(inv_perm) || !aligned16(d_rows) ||
       !aligned16(d_gates) || (gates && !aligned16(gates)))
     return MOE_ERR_MISALIGNED;
   const int64_t nb = T * D * 2;
+  if (T * k * D >= (int64_t(1) << 61)) return MOE_ERR_UNSUPPORTED;
   if (overlap(d_rows, nb * k, rows, nb * k) || overlap(d_rows, nb * k, dy, nb))
     return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_combine_bwd(dy, rows, inv_perm, gates, static_cast<int>(T), k, D, d_rows,

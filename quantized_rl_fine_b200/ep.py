@@ -33,6 +33,7 @@ from dataclasses import dataclass
 import torch
 import torch.distributed as dist
 
+from . import layer
 from . import moeq as M
 from .synth import QWeightT
 
@@ -90,23 +91,30 @@ class Dispatch:
     recv: list[int] | None = None             # rows received from each rank
 
 
-def route(x: torch.Tensor, logits: torch.Tensor, k: int, chunk_size: int, world: int) -> Dispatch:
+def route(x: torch.Tensor, logits: torch.Tensor, k: int, chunk_size: int, world: int,
+          router: M.RouterSpec | None = None, bias: torch.Tensor | None = None) -> Dispatch:
     """Phase 1: route this rank's tokens over all experts."""
-    r = M.moe_route_permute(logits, x, k, chunk_size)
+    r = layer.route(logits, x, k, chunk_size, router, bias)
     E = logits.shape[1]
     counts = (r.expert_offsets[1:] - r.expert_offsets[:-1]).to(torch.int32)
     return Dispatch(routing=r, counts=counts, send=send_splits(r.expert_offsets.cpu(), E, world))
 
 
-def expert_compute(rows: torch.Tensor, recv_counts: torch.Tensor, w_gu: QWeightT, w_d: QWeightT,
-                   chunk_size: int, adapter: torch.Tensor | None = None) -> torch.Tensor:
+def expert_compute(rows: torch.Tensor, recv_counts: torch.Tensor, w_gu: QWeightT | M.Fp8WeightT,
+                   w_d: QWeightT | M.Fp8WeightT, chunk_size: int, adapter: torch.Tensor | None = None) -> torch.Tensor:
     """Phase 2 on the owner: received rows (source-major) -> local expert-major
     -> gate/up + SwiGLU -> down -> back to source-major order."""
     if rows.shape[0] == 0:                      # no token chose this rank's experts
         return rows.new_empty((0, w_d.N))
     xl, groups = M.moe_ep_regroup(recv_counts, rows, 0, chunk_size)
-    h, _ = M.moe_grouped_qgemm_fwd(xl, w_gu, groups, M.EPI_SWIGLU, adapter=adapter)
-    yl = M.moe_grouped_qgemm_fwd(h, w_d, groups, M.EPI_NONE)
+    if isinstance(w_gu, M.Fp8WeightT):
+        if adapter is not None:
+            raise ValueError("FP8 experts take no adapter")
+        h, _ = M.moe_grouped_fp8_gemm_fwd(M.moe_quantize_fp8_rows(xl), w_gu, groups, M.EPI_SWIGLU)
+        yl = M.moe_grouped_fp8_gemm_fwd(h, w_d, groups)
+    else:
+        h, _ = M.moe_grouped_qgemm_fwd(xl, w_gu, groups, M.EPI_SWIGLU, adapter=adapter)
+        yl = M.moe_grouped_qgemm_fwd(h, w_d, groups, M.EPI_NONE)
     return M.moe_ep_regroup(recv_counts, yl, 1)
 
 
@@ -115,13 +123,14 @@ def combine(dsp: Dispatch, y_perm: torch.Tensor, T: int) -> torch.Tensor:
     return M.moe_unpermute_combine(y_perm, dsp.routing, dsp.routing.gates, T, mode=0)
 
 
-def forward(x: torch.Tensor, logits: torch.Tensor, w_gu_local: QWeightT, w_d_local: QWeightT,
-            k: int, chunk_size: int, adapter_local: torch.Tensor | None = None,
-            group=None) -> torch.Tensor:
+def forward(x: torch.Tensor, logits: torch.Tensor, w_gu_local: QWeightT | M.Fp8WeightT,
+            w_d_local: QWeightT | M.Fp8WeightT, k: int, chunk_size: int,
+            adapter_local: torch.Tensor | None = None, group=None, router: M.RouterSpec | None = None,
+            bias: torch.Tensor | None = None) -> torch.Tensor:
     """The layer forward with the experts split over the ranks of `group`;
     w_*_local hold this rank's E/W experts. Returns y for this rank's tokens."""
     world = dist.get_world_size(group) if dist.is_initialized() else 1
-    dsp = route(x, logits, k, chunk_size, world)
+    dsp = route(x, logits, k, chunk_size, world, router, bias)
     dsp.recv_counts = exchange_counts(dsp.counts, world, group)
     dsp.recv = dsp.recv_counts.sum(dim=1).cpu().tolist()
     rows = exchange_rows(dsp.routing.x_perm, dsp.send, dsp.recv, group)

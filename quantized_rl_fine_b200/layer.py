@@ -13,6 +13,13 @@ and the gate/up GEMM reads it through its tensor map; gather=True makes the
 GEMM gather the rows itself instead (same bits; at 341 rows per expert on
 B200 its gathering producer is about 2.2x slower than the tensor-map copy,
 because each stage is handed over only once its row copies have landed).
+
+router=RouterSpec(...) routes by scores (moe_route_scored, with an optional
+selection bias) and makes backward return the gradients of the gates and of
+the logits as well. With FP8 expert weights (Fp8WeightT) the products run in
+FP8: the token rows are quantized once and written in expert order, gate/up
+writes h as FP8 rows and gate|up as an 8-bit checkpoint, and the backward
+reads that checkpoint; no BF16 gate|up is kept.
 """
 
 from __future__ import annotations
@@ -23,26 +30,64 @@ from . import moeq as M
 from .synth import QWeightT
 
 
-def forward(x: torch.Tensor, logits: torch.Tensor, w_gu: QWeightT, w_d: QWeightT, k: int,
-            chunk_size: int, adapter: torch.Tensor | None = None, train: bool = False,
-            stream=None, gather: bool | None = None) -> dict:
+def route(logits: torch.Tensor, x: torch.Tensor | None, k: int, chunk_size: int,
+          router: M.RouterSpec | None = None, bias: torch.Tensor | None = None, stream=None) -> M.Routing:
+    """Softmax over the selected logits, or the scored routing when a router is given."""
+    if router is not None:
+        return M.moe_route_scored(logits, x, k, chunk_size, router, bias=bias, stream=stream)
+    if bias is not None:
+        raise ValueError("a selection bias needs a router (RouterSpec)")
+    return M.moe_route_permute(logits, x, k, chunk_size, stream=stream)
+
+
+def forward(x: torch.Tensor, logits: torch.Tensor, w_gu: QWeightT | M.Fp8WeightT,
+            w_d: QWeightT | M.Fp8WeightT, k: int, chunk_size: int, adapter: torch.Tensor | None = None,
+            train: bool = False, stream=None, gather: bool | None = None,
+            router: M.RouterSpec | None = None, bias: torch.Tensor | None = None) -> dict:
     T = x.shape[0]
+    scored = dict(router=router, logits=logits if router is not None else None)
+    if isinstance(w_gu, M.Fp8WeightT):
+        if adapter is not None or gather:
+            raise ValueError("FP8 experts take neither an adapter nor gather (their rows are written quantized)")
+        r = route(logits, None, k, chunk_size, router, bias, stream)
+        a = M.moe_quantize_fp8_rows(x, r, stream=stream)
+        h, saved = M.moe_grouped_fp8_gemm_fwd(a, w_gu, r, M.EPI_SWIGLU, save_gu=train, stream=stream)
+        y_perm = M.moe_grouped_fp8_gemm_fwd(h, w_d, r, stream=stream)
+        y = M.moe_unpermute_combine(y_perm, r, r.gates, T, mode=0, stream=stream)
+        return dict(routing=r, x=x, a=a, a_rows=None, h=h, saved_gu=saved, y_perm=y_perm, y=y, **scored)
     if gather is None:
         gather = adapter is not None
-    r = M.moe_route_permute(logits, None if gather else x, k, chunk_size, stream=stream)
+    r = route(logits, None if gather else x, k, chunk_size, router, bias, stream)
     a, a_rows = (x, r.perm_token) if gather else (r.x_perm, None)
     h, saved = M.moe_grouped_qgemm_fwd(a, w_gu, r, M.EPI_SWIGLU, adapter=adapter,
                                        save_gu=train, stream=stream, a_rows=a_rows)
     y_perm = M.moe_grouped_qgemm_fwd(h, w_d, r, M.EPI_NONE, stream=stream)
     y = M.moe_unpermute_combine(y_perm, r, r.gates, T, mode=0, stream=stream)
-    return dict(routing=r, x=x, a=a, a_rows=a_rows, h=h, saved_gu=saved, y_perm=y_perm, y=y)
+    return dict(routing=r, x=x, a=a, a_rows=a_rows, h=h, saved_gu=saved, y_perm=y_perm, y=y, **scored)
 
 
-def backward(state: dict, dy: torch.Tensor, w_gu: QWeightT, w_d: QWeightT,
+def backward(state: dict, dy: torch.Tensor, w_gu: QWeightT | M.Fp8WeightT, w_d: QWeightT | M.Fp8WeightT,
              adapter: torch.Tensor | None = None, stream=None) -> dict:
+    """Gradients of the step; with a router also d_gates [T, k] and d_logits [T, E]."""
     r: M.Routing = state["routing"]
     T = dy.shape[0]
-    dy_perm = M.moe_unpermute_combine(dy, r, r.gates, T, mode=1, stream=stream)
+    d_gates = d_logits = None
+    if state.get("router") is not None:
+        dy_perm, d_gates = M.moe_combine_bwd(dy, state["y_perm"], r, stream=stream)
+        d_logits = M.moe_route_scored_bwd(d_gates, state["logits"], r, state["router"], stream=stream)
+    else:
+        dy_perm = M.moe_unpermute_combine(dy, r, r.gates, T, mode=1, stream=stream)
+    if isinstance(w_gu, M.Fp8WeightT):
+        if adapter is not None:
+            raise ValueError("FP8 experts take no adapter")
+        if state["saved_gu"] is None:
+            raise ValueError("backward needs a forward with train=True")
+        d = M.moe_quantize_fp8_rows(dy_perm, stream=stream)
+        dgu = M.moe_grouped_fp8_gemm_bwd_dx(d, w_d, r, M.EPI_SWIGLU_BWD, saved=state["saved_gu"], stream=stream)
+        dx_perm = M.moe_grouped_fp8_gemm_bwd_dx(dgu, w_gu, r, stream=stream)
+        dx = M.moe_unpermute_combine(dx_perm, r, None, T, mode=0, stream=stream)
+        return dict(dy_perm=dy_perm, dgu=dgu, dx_perm=dx_perm, dx=dx, d_adapter=None, d_gates=d_gates,
+                    d_logits=d_logits)
     dgu = M.moe_grouped_qgemm_bwd_dx(dy_perm, w_d, r, M.EPI_SWIGLU_BWD, saved_gu=state["saved_gu"],
                                      stream=stream)
     if adapter is not None:
@@ -53,7 +98,8 @@ def backward(state: dict, dy: torch.Tensor, w_gu: QWeightT, w_d: QWeightT,
         dx_perm = M.moe_grouped_qgemm_bwd_dx(dgu, w_gu, r, M.EPI_NONE, stream=stream)
         d_adapter = None
     dx = M.moe_unpermute_combine(dx_perm, r, None, T, mode=0, stream=stream)
-    return dict(dy_perm=dy_perm, dgu=dgu, dx_perm=dx_perm, dx=dx, d_adapter=d_adapter)
+    return dict(dy_perm=dy_perm, dgu=dgu, dx_perm=dx_perm, dx=dx, d_adapter=d_adapter, d_gates=d_gates,
+                d_logits=d_logits)
 
 
 def up_projection(x: torch.Tensor, logits: torch.Tensor, w_up: QWeightT, k: int, chunk_size: int,

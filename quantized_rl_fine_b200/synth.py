@@ -73,6 +73,20 @@ def quantize_mxfp4(w: torch.Tensor):
     return _pack_codes(code.reshape(*lead, N, K)), X.to(torch.uint8).transpose(-1, -2).contiguous()
 
 
+def quantize_fp8(w: torch.Tensor):
+    """FP8 expert weights: e4m3 elements, one fp32 scale amax / 448 per 128 x 128 block (1 for a
+    block of zeros). Returns (q float8_e4m3fn [..., N, K], scales float32 [..., ceil(N/128), ceil(K/128)])."""
+    *lead, N, K = w.shape
+    nb, kb = -(-N // 128), -(-K // 128)
+    p = torch.zeros((*lead, nb * 128, kb * 128), dtype=torch.float32, device=w.device)
+    p[..., :N, :K] = w
+    b = p.reshape(*lead, nb, 128, kb, 128)
+    s = b.abs().amax((-3, -1)) / 448.0
+    s = torch.where(s == 0, torch.ones_like(s), s)
+    q = (b / s[..., :, None, :, None]).reshape(*lead, nb * 128, kb * 128)[..., :N, :K]
+    return q.clamp(-448.0, 448.0).to(torch.float8_e4m3fn).contiguous(), s
+
+
 def quantize(w: torch.Tensor, fmt: str):
     if fmt == "int4":
         return quantize_int4(w)
