@@ -96,6 +96,26 @@ __global__ void scatter_kernel(const uint4* __restrict__ rows, const int32_t* __
   }
 }
 
+// bf16_of_product of eight values at once: the halfway case, one product in
+// 65536, is looked for in all eight together.
+__device__ __forceinline__ uint4 bf16_of_products8(float g, const float (&x)[8]) {
+  float p[8];
+  uint32_t nearest = 0xffffffffu;          // smallest distance of a product's low half from 0x8000
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    p[i] = g * x[i];
+    nearest = min(nearest, (__float_as_uint(p[i]) & 0xFFFFu) ^ 0x8000u);
+  }
+  if (nearest == 0u) {
+    uint32_t h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = bf16_of_product(g, x[i]);
+    return make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+  }
+  return make_uint4(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]),
+                    pack_bf16x2(p[6], p[7]));
+}
+
 // One block per token, 16-byte slices of the row over its threads: dy is read
 // once, each of the token's k rows once, and gate * dy written once to each of
 // the k slots (bf16_of_product: one rounding, the bits of scatter_kernel). The
@@ -121,10 +141,10 @@ combine_bwd_kernel(const uint4* __restrict__ dy, const uint4* __restrict__ rows,
   }
   for (int64_t c = threadIdx.x; c < dvec; c += blockDim.x) {
     uint4 r[KMAX];
-    const uint4 dv = __ldg(dy + t * dvec + c);
+    const uint4 dv = __ldcs(dy + t * dvec + c);
 #pragma unroll
     for (int j = 0; j < KMAX; ++j)
-      if (j < k) r[j] = __ldg(rows + base[j] + c);
+      if (j < k) r[j] = __ldcs(rows + base[j] + c);
     float f[8];
     unpack8(dv, f);
 #pragma unroll
@@ -132,14 +152,9 @@ combine_bwd_kernel(const uint4* __restrict__ dy, const uint4* __restrict__ rows,
       if (j >= k) continue;
       float y[8];
       unpack8(r[j], y);
-      uint32_t h[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        acc[j] = fmaf(f[i], y[i], acc[j]);
-        h[i] = bf16_of_product(g[j], f[i]);
-      }
-      d_rows[base[j] + c] = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16),
-                                       h[6] | (h[7] << 16));
+      for (int i = 0; i < 8; ++i) acc[j] = fmaf(f[i], y[i], acc[j]);
+      __stcs(d_rows + base[j] + c, bf16_of_products8(g[j], f));
     }
   }
 #pragma unroll

@@ -18,18 +18,47 @@ __device__ __forceinline__ void bf16x16(const uint4& u, const uint4& v, float (&
   }
 }
 
-// One block per token. A thread takes 16 elements (two 16-byte loads); the
-// eight threads of a 128-element block find its largest magnitude with three
-// shuffles. The token is read and quantized once and written to its k rows
-// (16-byte stores), which costs k writes of one byte an element against k
-// reads of two if every permuted row were quantized by itself.
+// Sixteen BF16 values (two 16-byte pieces) of a 128-element block to e4m3; the
+// block's eight threads find its largest magnitude with three shuffles.
+__device__ __forceinline__ uint4 quantize16(const uint4& a, const uint4& b, float* scale) {
+  float f[16];
+  bf16x16(a, b, f);
+  float amax = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(f[j]));     // (NaN is passed over)
+  if (!(amax < INFINITY)) {                                          // rare
+    amax = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) amax = fmaxf(amax, finite_abs(f[j]));
+#pragma unroll
+    for (int j = 0; j < 16; ++j) f[j] = inf_to_nan(f[j]);
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const int e = fp8_block_exp(amax);
+  const float inv = exp2_int(-e);
+  *scale = exp2_int(e);
+  return make_uint4(cvt_e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
+                    cvt_e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv),
+                    cvt_e4m3x4(f[8] * inv, f[9] * inv, f[10] * inv, f[11] * inv),
+                    cvt_e4m3x4(f[12] * inv, f[13] * inv, f[14] * inv, f[15] * inv));
+}
+
+// A group of 8 / TPB warps per token, TPB tokens a block: each thread takes 16
+// elements at a time, two such units in flight. The token is read and
+// quantized once and written to its k rows (16-byte stores), which costs k
+// writes of one byte an element against k reads of two if every permuted row
+// were quantized by itself. Bound: DRAM, read once and written k times.
+template <int TPB>
 __global__ void __launch_bounds__(256)
-quantize_fp8_kernel(const uint4* __restrict__ x, int64_t K, const int32_t* __restrict__ inv_perm,
+quantize_fp8_kernel(const uint4* __restrict__ x, int T, int64_t K, const int32_t* __restrict__ inv_perm,
                     int k, int M, uint8_t* __restrict__ q, float* __restrict__ scales) {
   grid_dependency_wait();
   grid_dependents_launch();
-  const int64_t t = blockIdx.x;
-  const int lane = threadIdx.x & 31;
+  constexpr int kLanes = 256 / TPB;                           // threads of a token
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * TPB + threadIdx.x / kLanes;
+  if (t >= T) return;                                         // whole warps
+  const int th = threadIdx.x % kLanes, lane = threadIdx.x & 31;
   // Lane j < k holds the token's j-th row (-1: not a row).
   int my_row = -1;
   if (lane < k) {
@@ -37,52 +66,38 @@ quantize_fp8_kernel(const uint4* __restrict__ x, int64_t K, const int32_t* __res
     if (my_row < 0 || my_row >= M) my_row = -1;
   }
   const int units = static_cast<int>(K / 16);
-  const int steps = (units + blockDim.x - 1) / blockDim.x;    // uniform: every thread shuffles
-  for (int i = 0; i < steps; ++i) {
-    const int un = i * blockDim.x + threadIdx.x;
-    const bool ok = un < units;
-    float f[16];
-    {
-      uint4 a = make_uint4(0, 0, 0, 0), b = a;
-      if (ok) {
-        const uint4* src = x + t * (K / 8) + 2 * un;
-        a = __ldg(src);
-        b = __ldg(src + 1);
-      }
-      bf16x16(a, b, f);
-    }
-    float amax = 0.0f;
-    bool odd = false;                       // holds a value that is not finite
+  const uint4* src = x + t * (K / 8);
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int base = 0; base < units; base += 2 * kLanes) {      // uniform over the warp: every lane shuffles
+    uint4 v[2][2], o[2];
+    float sc[2];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      amax = fmaxf(amax, finite_abs(f[j]));
-      odd |= !(fabsf(f[j]) < INFINITY);
+    for (int i = 0; i < 2; ++i) {
+      const int un = base + i * kLanes + th;
+      v[i][0] = un < units ? __ldcs(src + 2 * un) : zero;
+      v[i][1] = un < units ? __ldcs(src + 2 * un + 1) : zero;
     }
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const int e = fp8_block_exp(amax);
-    const float inv = exp2_int(-e);
-    if (odd) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) f[j] = inf_to_nan(f[j]);
-    }
-    uint4 o;
-    o.x = cvt_e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
-    o.y = cvt_e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
-    o.z = cvt_e4m3x4(f[8] * inv, f[9] * inv, f[10] * inv, f[11] * inv);
-    o.w = cvt_e4m3x4(f[12] * inv, f[13] * inv, f[14] * inv, f[15] * inv);
-    const float sc = exp2_int(e);
+    for (int i = 0; i < 2; ++i) o[i] = quantize16(v[i][0], v[i][1], &sc[i]);
     for (int j = 0; j < k; ++j) {
       const int64_t r = __shfl_sync(0xffffffffu, my_row, j);
-      if (!ok || r < 0) continue;
-      *reinterpret_cast<uint4*>(q + r * K + 16 * un) = o;
-      if ((un & 7) == 0) scales[static_cast<int64_t>(un >> 3) * M + r] = sc;
+      if (r < 0) continue;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int un = base + i * kLanes + th;
+        if (un >= units) continue;
+        *reinterpret_cast<uint4*>(q + r * K + 16ll * un) = o[i];
+        if ((un & 7) == 0) scales[static_cast<int64_t>(un >> 3) * M + r] = sc[i];
+      }
     }
   }
 }
 
-// Blocks of 8 rows x 32 units of 16 elements, one row a warp: the rows' scales
-// of a block column lie next to each other and share their memory sectors.
+// Blocks of 8 rows x 1024 elements, one row a warp: the rows' scales of a block
+// column lie next to each other and share their memory sectors. Eight elements
+// a lane and step, so that both the loads (8 bytes) and the stores (16) of a
+// warp are contiguous: 16 elements a lane, two stores 32 bytes apart, wrote
+// every sector in halves (32768 x 4096: 83 us). Bound: DRAM.
 template <int FMT>
 __global__ void __launch_bounds__(256)
 dequantize_fp8_kernel(const uint8_t* __restrict__ q, const void* __restrict__ scales, int M, int64_t K,
@@ -91,28 +106,31 @@ dequantize_fp8_kernel(const uint8_t* __restrict__ q, const void* __restrict__ sc
   grid_dependents_launch();
   const int64_t m = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  const int units = static_cast<int>(K / 16);
+  const int units = static_cast<int>(K / 8);
   if (m >= M) return;
-  for (int un = blockIdx.y * 32 + lane; un < units; un += 32 * gridDim.y) {
-    float s;
-    if constexpr (FMT == MOE_FP8_BLOCK128_F32) {
-      s = __ldg(static_cast<const float*>(scales) + static_cast<int64_t>(un >> 3) * M + m);
-    } else {
-      const int X = __ldg(static_cast<const uint8_t*>(scales) + static_cast<int64_t>(un >> 1) * M + m);
-      s = e8m0_to_float(X);
-    }
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(q + m * K) + un);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t o[8];
+  for (int base = blockIdx.y * 128; base < units; base += 128 * gridDim.y) {
+    uint2 v[4];
+    float s[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 lo = e4m3x2_to_float2(w[i]), hi = e4m3x2_to_float2(w[i] >> 16);
-      o[2 * i] = pack_bf16x2(lo.x * s, lo.y * s);
-      o[2 * i + 1] = pack_bf16x2(hi.x * s, hi.y * s);
+      const int un = base + 32 * i + lane;
+      if (un >= units) continue;
+      v[i] = __ldcs(reinterpret_cast<const uint2*>(q + m * K) + un);
+      if constexpr (FMT == MOE_FP8_BLOCK128_F32)
+        s[i] = __ldg(static_cast<const float*>(scales) + static_cast<int64_t>(un >> 4) * M + m);
+      else
+        s[i] = e8m0_to_float(__ldg(static_cast<const uint8_t*>(scales) + static_cast<int64_t>(un >> 2) * M + m));
     }
-    uint4* dst = reinterpret_cast<uint4*>(out + m * K) + 2 * un;
-    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int un = base + 32 * i + lane;
+      if (un >= units) continue;
+      const float2 a = e4m3x2_to_float2(v[i].x), b = e4m3x2_to_float2(v[i].x >> 16);
+      const float2 c = e4m3x2_to_float2(v[i].y), d = e4m3x2_to_float2(v[i].y >> 16);
+      __stcs(reinterpret_cast<uint4*>(out + m * K) + un,
+             make_uint4(pack_bf16x2(a.x * s[i], a.y * s[i]), pack_bf16x2(b.x * s[i], b.y * s[i]),
+                        pack_bf16x2(c.x * s[i], c.y * s[i]), pack_bf16x2(d.x * s[i], d.y * s[i])));
+    }
   }
 }
 
@@ -120,14 +138,19 @@ dequantize_fp8_kernel(const uint8_t* __restrict__ q, const void* __restrict__ sc
 
 cudaError_t launch_quantize_fp8_rows(const void* x, int T, int64_t K, const int32_t* inv_perm, int k,
                                      void* q, float* scales, cudaStream_t s) {
-  const int threads = static_cast<int>(std::min<int64_t>(256, (K / 16 + 31) / 32 * 32));
-  return launch_pdl(quantize_fp8_kernel, dim3(T), dim3(threads), 0, s, static_cast<const uint4*>(x), K,
+  // A warp per token when there are enough tokens to fill the SMs that way and
+  // each is written once (32768 x 7168: 113 us, 150 with a block per token);
+  // a block per token for few tokens (latency), and when a token is written to
+  // k rows (4096 x 7168 to 8 rows: 60 us, 73 with a warp per token).
+  const int tpb = K <= 512 || (T >= 4096 && k == 1) ? 8 : 1;
+  auto kern = tpb == 8 ? quantize_fp8_kernel<8> : quantize_fp8_kernel<1>;
+  return launch_pdl(kern, dim3((T + tpb - 1) / tpb), dim3(256), 0, s, static_cast<const uint4*>(x), T, K,
                     inv_perm, k, T * k, static_cast<uint8_t*>(q), scales);
 }
 
 cudaError_t launch_dequantize_fp8_rows(const void* q, const void* scales, int M, int64_t K, int fmt,
                                        void* out, cudaStream_t s) {
-  const int64_t cols = (K / 16 + 31) / 32;
+  const int64_t cols = (K / 8 + 127) / 128;
   const dim3 grid((M + 7) / 8, static_cast<unsigned>(std::min<int64_t>(cols, 65535)));
   auto kern = fmt == MOE_FP8_BLOCK128_F32 ? dequantize_fp8_kernel<MOE_FP8_BLOCK128_F32>
                                           : dequantize_fp8_kernel<MOE_FP8_BLOCK32_E8M0>;
