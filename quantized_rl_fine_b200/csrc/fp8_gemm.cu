@@ -43,15 +43,15 @@ constexpr int kEpiWarp8 = 4;             // warp 0 copies, warp 1 issues MMAs, w
 constexpr int kEpiWarps8 = 8;
 constexpr int kThreads8 = 32 * (kEpiWarp8 + kEpiWarps8);
 // Registers: 168 a thread at launch (384 x 168 = 64512); the first warpgroup
-// gives up 128 a thread and the two epilogue warpgroups take 64 each: 128 x 40
-// + 256 x 232 = 64512. An epilogue thread holds 128 accumulators and 64 values in flight.
-constexpr int kRegsCopy = 40, kRegsEpi = 232;
+// gives up 96 a thread and the two epilogue warpgroups take 48 each: 128 x 72
+// + 256 x 216 = 64512. An epilogue thread holds 128 accumulators and 64 values in flight.
+constexpr int kRegsCopy = 72, kRegsEpi = 216;
 static_assert(128 * kRegsCopy + 256 * kRegsEpi <= kThreads8 * 168, "register split");
 // Output staging of one epilogue thread: its 256 bytes of a row, padded so
 // that the 16-byte stores of eight neighbouring threads fall in distinct banks.
 constexpr uint32_t kSlot8 = 272;
 constexpr size_t smem_bytes8(int E, int pair) {
-  return 1024 + stages8(pair) * stage_bytes8(pair) + 256 * kSlot8 + 8 * (2 * stages8(pair) + 8) + 16 + 4 * 4 * kRows8 + 4 * 32 +
+  return 1024 + stages8(pair) * stage_bytes8(pair) + 256 * kSlot8 + 8 * (2 * stages8(pair) + 10) + 16 + 4 * 4 * kRows8 + 4 * 32 +
          4 * 2 * (static_cast<size_t>(E) + 1) + 2 * static_cast<size_t>(E);
 }
 static_assert(smem_bytes8(1024, 0) <= 227 * 1024 && smem_bytes8(1024, 1) <= 227 * 1024, "shared memory of the largest stack");
@@ -315,6 +315,14 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
   return v;
 }
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t a) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(a) : "memory");
+}
 __device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
@@ -352,9 +360,10 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
   const uint32_t amax_bar = bars + 8u * (2 * S + 5);
   const uint32_t gu_bar = bars + 8u * (2 * S + 6);
   const uint32_t slot_free = bars + 8u * (2 * S + 7);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (bars - base) + 8u * (2 * S + 8));
+  auto sc_free = [&](int b) { return bars + 8u * (2 * S + 8 + b); };   // scales of buffer b have been read
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (bars - base) + 8u * (2 * S + 10));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const uint32_t abort_at = bars + 8u * (2 * S + 8) + 4u;
+  const uint32_t abort_at = bars + 8u * (2 * S + 10) + 4u;
   float* row_amax = reinterpret_cast<float*>(tmem_slot + 4);                 // [2 tiles][2][128]
   int32_t* warp_tot = reinterpret_cast<int32_t*>(row_amax + 4 * kRows8);     // [32]
   TileList8 list;
@@ -373,8 +382,9 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
       mbar_init(empty(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(acc_full(b), 1);
+      mbar_init(acc_full(b), 2);               // the MMAs' commit and the scale warp
       mbar_init(acc_empty(b), kEpiWarps8 << PAIR);
+      mbar_init(sc_free(b), kEpiWarps8);
     }
     mbar_init(drain_bar, 1);
     mbar_init(amax_bar, kEpiWarps8);
@@ -489,6 +499,73 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
     __syncwarp();
     if (lane == 0) mbar_drain(drain_bar, 0);
     __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ scales
+    // Forms each reduction block's factors (row scale times weight scale) two
+    // blocks ahead and hands them over with the accumulator buffer, in the
+    // padding of the epilogue threads' slots. Loaded by the epilogue threads
+    // themselves one block ahead, they bounded the product: a block took as
+    // long as such a load, about 1000 cycles, however few columns it had.
+    bool ok = true;
+    uint32_t it = 0;
+    Tile8 tl;
+    tl.a = 0;
+    for (int t = t_first; t < total && ok; t += t_step) {
+      tl = tile8_at<PAIR>(list, t, tl.a, rank);
+      // Blocks past the last feature (a tile that ends early) are clamped;
+      // their columns are not stored.
+      const float* pw = p.w_scales + static_cast<int64_t>(tl.e) * p.NB * p.KB;
+      int64_t up = 0;                        // from the first to the second half's weight block
+      if constexpr (BWD) {
+        pw += tl.ft * 2;
+        up = min(tl.ft * 2 + 1, p.KB - 1) - tl.ft * 2;
+      } else if constexpr (kGlu) {
+        pw += static_cast<int64_t>(tl.ft) * p.KB;
+        up = static_cast<int64_t>(f_half / 128) * p.KB;
+      } else {
+        pw += static_cast<int64_t>(tl.ft * 2) * p.KB;
+        up = static_cast<int64_t>(min(tl.ft * 2 + 1, p.NB - 1) - tl.ft * 2) * p.KB;
+      }
+      const float* pa = p.a_scales;
+      int off[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) off[i] = min(tl.row0 + 32 * i + lane, p.M - 1);
+      struct Set {
+        float a[4], w0, w1;
+      } set[2];
+      auto fetch = [&](Set& x) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x.a[i] = __ldg(pa + off[i]);
+        x.w0 = __ldg(pw);
+        x.w1 = __ldg(pw + up);
+        pa += p.M;
+        pw += BWD ? p.KB : 1;
+      };
+      auto step = [&](Set& x, int kb) {
+        const int b = static_cast<int>(it & 1);
+        ok = mbar_wait8(sc_free(b), ((it >> 1) & 1) ^ 1u, abort_at);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t pad = stg_base + static_cast<uint32_t>(i * 32 + lane) * kSlot8 + 256u;
+          if constexpr (kGlu)
+            sts64(pad + 8u * b, __float_as_uint(x.a[i & 3] * x.w0), __float_as_uint(x.a[i & 3] * x.w1));
+          else
+            sts32(pad + (kGluBwd ? 8u : 0u) + 4u * b, __float_as_uint(x.a[i & 3] * (i < 4 ? x.w0 : x.w1)));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_full(b));
+        if (kb + 2 < p.nkb) fetch(x);
+        ++it;
+      };
+      fetch(set[0]);
+      if (p.nkb > 1) fetch(set[1]);
+      for (int kb = 0; kb < p.nkb && ok; kb += 2) {
+        step(set[0], kb);
+        if (ok && kb + 1 < p.nkb) step(set[1], kb + 1);
+      }
+    }
   } else if (kGluBwd && warp == 3) {
     // ------------------------------------------------------------ checkpoint rows
     // For the 256 staging slots (row, half) of each tile: the row's 128 bytes
@@ -546,42 +623,19 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
     const uint32_t col0 = static_cast<uint32_t>(kGlu ? wg * 64 : wg * 128);
     const uint32_t col1 = col0 + (kGlu ? 128u : 64u);
     // Registers are what this loop is short of (128 accumulators, 64 values in
-    // flight, 232 a thread), and a spill in it costs more than anything else
-    // here, so its state is few words: the tile as (row or -1, ft, a), and
-    // pointers that step through the scales of the reduction blocks: the row's
-    // (stride M) and the weight blocks' of the two column halves (stride
-    // w_step; SwiGLU's up block w_up further on).
-    const int64_t w_up = static_cast<int64_t>(f_half / 128) * p.KB;
-    const float* pa;
-    const float* pw;
-    int row, ft, ta = 0;
-    float na = 0.0f, n0 = 0.0f, n1 = 0.0f;       // scales of the next reduction block
-    // Blocks past the last feature (a tile that ends early) are clamped; their
-    // columns are not stored.
+    // flight, 216 a thread), and a spill in it costs more than anything else
+    // here: the tile is kept as (row or -1, ft, a).
+    int row = -1, ft = 0, ta = 0;
     auto enter = [&](int t) {
       const Tile8 tl = tile8_at<PAIR>(list, t, ta, rank);
       ta = tl.a;
       ft = tl.ft;
       row = tl.row0 + r_in;
-      pa = p.a_scales + min(row, p.M - 1);
       if (row >= tl.row_end) row = -1;
-      pw = p.w_scales + static_cast<int64_t>(tl.e) * p.NB * p.KB;
-      if constexpr (BWD) pw += min(ft * 2 + wg, p.KB - 1);
-      else pw += static_cast<int64_t>(kGlu ? ft : min(ft * 2 + wg, p.NB - 1)) * p.KB;
-    };
-    auto fetch = [&]() {
-      na = __ldg(pa);
-      n0 = __ldg(pw);
-      if constexpr (kGlu) n1 = __ldg(pw + w_up);
-      pa += p.M;
-      pw += BWD ? p.KB : 1;
     };
     uint32_t it = 0;                             // reduction blocks so far (buffer it % 2)
     uint32_t li = 0;                             // parity of this CTA's tile count
-    if (t_first < total) {
-      enter(t_first);
-      fetch();
-    }
+    if (t_first < total) enter(t_first);
     for (int t = t_first; t < total; t += t_step, li ^= 1u) {
       const int cur_row = row, cur_ft = ft;
       uint64_t acc2[64];
@@ -598,14 +652,6 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
             if (lane == 0) mbar_arrive(slot_free);
           }
         }
-        const float s0 = na * n0, s1 = kGlu ? na * n1 : s0;
-        if (kb + 1 < p.nkb) {
-          fetch();
-        } else if (t + t_step < total) {
-          // the next tile's first scales arrive during this tile's epilogue
-          enter(t + t_step);
-          fetch();
-        }
         const int b = static_cast<int>(it & 1);
         const bool r = mbar_wait8(acc_full(b), static_cast<uint32_t>((it >> 1) & 1), abort_at);
         if (!__shfl_sync(0xffffffffu, r ? 1 : 0, 0)) { ok = false; break; }
@@ -616,6 +662,14 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
         uint32_t v0[32], v1[32];
         tmem_ld_32x32b_x32(tb + col0, v0);
         tmem_ld_32x32b_x32(tb + col0 + 32u, v1);
+        float s0, s1;
+        if constexpr (kGlu) {
+          const uint2 sc = lds64(slot + 256u + 8u * b);
+          s0 = __uint_as_float(sc.x);
+          s1 = __uint_as_float(sc.y);
+        } else {
+          s0 = s1 = __uint_as_float(lds32(slot + 256u + (kGluBwd ? 8u : 0u) + 4u * b));
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           tmem_wait_ld();
@@ -625,6 +679,7 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
             if (lane == 0) {
               if constexpr (PAIR) arrive_remote(cluster_addr(acc_empty(b), 0));
               else mbar_arrive(acc_empty(b));
+              mbar_arrive(sc_free(b));
             }
           }
           const float s = h ? s1 : s0;
@@ -642,6 +697,7 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
         ok = __all_sync(0xffffffffu, ok);
       }
       if (!ok) break;
+      if (t + t_step < total) enter(t + t_step);
       [[maybe_unused]] float acc[128];
       if constexpr (!kGluBwd) {
 #pragma unroll
