@@ -355,8 +355,12 @@ moe_status moe_route_scored(const float* logits, const float* bias, const void* 
 /*
  * moe_route_scored_bwd -- gradient of the gates with respect to the logits.
  * The selection and the bias get none (the selection is piecewise constant).
- *  d_gates   [T][k] fp32, topk_idx [T][k] int32 as moe_route_scored wrote it
- *            (an id outside [0, E) contributes nothing), logits [T][E] fp32.
+ *  d_gates   [T][k] fp32, logits [T][E] fp32.
+ *  topk_idx  [T][k] int32 as moe_route_scored wrote it: a token's ids are
+ *            distinct (an id outside [0, E) contributes nothing).
+ *  gates     [T][k] fp32 as moe_route_scored wrote them, or NULL. A slot whose
+ *            gate is 0 contributes nothing: with a bias, that is how an expert
+ *            masked by its key is known here. NULL when no bias masks experts.
  *  d_logits  [T][E] fp32, every entry written.
  * With c = scale, s the scores, S the sum of the k selected ones:
  *   ds_j = c * d_gates_j, or with renorm c * (d_gates_j - sum_i d_gates_i s_i / S) / S
@@ -366,9 +370,9 @@ moe_status moe_route_scored(const float* logits, const float* bias, const void* 
  * 1 <= E <= 1024, 1 <= k <= min(E, 32). Only score, renorm and scale of
  * `router` are read.
  */
-moe_status moe_route_scored_bwd(const float* d_gates, const float* logits, const int32_t* topk_idx,
-                                int64_t T, int32_t E, int32_t k, const moe_router* router,
-                                float* d_logits, void* stream);
+moe_status moe_route_scored_bwd(const float* d_gates, const float* gates, const float* logits,
+                                const int32_t* topk_idx, int64_t T, int32_t E, int32_t k,
+                                const moe_router* router, float* d_logits, void* stream);
 
 /*
  * moe_combine_bwd -- backward of moe_unpermute_combine (mode 0) with respect
@@ -376,7 +380,8 @@ moe_status moe_route_scored_bwd(const float* d_gates, const float* logits, const
  *   d_rows[inv_perm[t*k+j]] = bf16(gates[t][j] * dy[t])   (as mode 1 writes it)
  *   d_gates[t][j] = sum_c dy[t][c] * rows[inv_perm[t*k+j]][c]   (fp32, fixed order)
  *  dy [T][D], rows and d_rows [T*k][D] bf16; d_rows must not overlap rows or
- *  dy. gates NULL: all ones. D % 8 == 0, 1 <= k <= 32.
+ *  dy. gates NULL: all ones. A slot whose inv_perm is outside [0, T*k) gets
+ *  d_gates 0 and writes no row. D % 8 == 0, 1 <= k <= 32.
  */
 moe_status moe_combine_bwd(const void* dy, const void* rows, const int32_t* inv_perm,
                            const float* gates, int64_t T, int32_t k, int64_t D, void* d_rows,

@@ -77,7 +77,8 @@ def route_scored(logits, k, score="softmax", groups=1, topk_groups=1, group_top=
     return idx, gates
 
 
-def route_scored_bwd(d_gates, logits, topk, score="softmax", renorm=True, scale=1.0):
+def route_scored_bwd(d_gates, logits, topk, score="softmax", renorm=True, scale=1.0, gates=None):
+    """gates (if given): slots whose gate is 0 are masked and contribute nothing."""
     d = np.asarray(d_gates, np.float64)
     s = scored_scores(logits, score)
     T, E = s.shape
@@ -85,6 +86,8 @@ def route_scored_bwd(d_gates, logits, topk, score="softmax", renorm=True, scale=
     for t in range(T):
         sel = [int(e) for e in topk[t]]
         w = np.array([s[t, e] for e in sel])
+        if gates is not None:
+            w = np.where(np.asarray(gates)[t] == 0, 0.0, w)
         dw = scale * np.where(w > 0, d[t], 0.0)
         if renorm:
             S = w.sum()
@@ -92,7 +95,7 @@ def route_scored_bwd(d_gates, logits, topk, score="softmax", renorm=True, scale=
         else:
             ds = dw
         full = np.zeros(E)
-        full[sel] = ds
+        full[sel] = np.where(w > 0, ds, 0.0)          # a masked expert's gate is the constant 0
         if score == "sigmoid":
             out[t] = full * s[t] * (1.0 - s[t])
         else:

@@ -871,8 +871,8 @@ moe_status moe_route_scored(const float* logits, const float* bias, const void* 
                                          static_cast<cudaStream_t>(stream)));
 }
 
-moe_status moe_route_scored_bwd(const float* d_gates, const float* logits, const int32_t* topk_idx,
-                                int64_t T, int32_t E, int32_t k, const moe_router* router,
+moe_status moe_route_scored_bwd(const float* d_gates, const float* gates, const float* logits,
+                                const int32_t* topk_idx, int64_t T, int32_t E, int32_t k, const moe_router* router,
                                 float* d_logits, void* stream) {
   MOEQ_TRACE("moe_route_scored_bwd");
   if (T < 1 || E < 1 || E > 1024 || k < 1 || k > 32 || k > E) return MOE_ERR_INVALID_ARG;
@@ -881,9 +881,10 @@ moe_status moe_route_scored_bwd(const float* d_gates, const float* logits, const
       (router->renorm != 0 && router->renorm != 1) || !std::isfinite(router->scale))
     return MOE_ERR_INVALID_ARG;
   if (!d_gates || !logits || !topk_idx || !d_logits) return MOE_ERR_INVALID_ARG;
-  if (!aligned16(d_gates) || !aligned16(logits) || !aligned16(topk_idx) || !aligned16(d_logits))
+  if (!aligned16(d_gates) || !aligned16(logits) || !aligned16(topk_idx) || !aligned16(d_logits) ||
+      (gates && !aligned16(gates)))
     return MOE_ERR_MISALIGNED;
-  return cuda_status(launch_route_scored_bwd(d_gates, logits, topk_idx, static_cast<int>(T), E, k,
+  return cuda_status(launch_route_scored_bwd(d_gates, gates, logits, topk_idx, static_cast<int>(T), E, k,
                                              *router, d_logits, static_cast<cudaStream_t>(stream)));
 }
 

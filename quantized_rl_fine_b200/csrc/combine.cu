@@ -135,7 +135,8 @@ combine_bwd_kernel(const uint4* __restrict__ dy, const uint4* __restrict__ rows,
   float g[KMAX], acc[KMAX];
 #pragma unroll
   for (int j = 0; j < KMAX; ++j) {
-    base[j] = (j < k) ? static_cast<int64_t>(__ldg(inv_perm + t * k + j)) * dvec : 0;
+    const int p = (j < k) ? __ldg(inv_perm + t * k + j) : -1;
+    base[j] = (p >= 0 && p < static_cast<int>(gridDim.x) * k) ? p * dvec : -1;
     g[j] = (j < k && gates) ? __ldg(gates + t * k + j) : 1.0f;
     acc[j] = 0.0f;
   }
@@ -144,12 +145,12 @@ combine_bwd_kernel(const uint4* __restrict__ dy, const uint4* __restrict__ rows,
     const uint4 dv = __ldcs(dy + t * dvec + c);
 #pragma unroll
     for (int j = 0; j < KMAX; ++j)
-      if (j < k) r[j] = __ldcs(rows + base[j] + c);
+      if (base[j] >= 0) r[j] = __ldcs(rows + base[j] + c);
     float f[8];
     unpack8(dv, f);
 #pragma unroll
     for (int j = 0; j < KMAX; ++j) {
-      if (j >= k) continue;
+      if (base[j] < 0) continue;
       float y[8];
       unpack8(r[j], y);
 #pragma unroll

@@ -860,8 +860,9 @@ cudaError_t launch_fp8_gemm_t(const CUtensorMap& ta, const CUtensorMap& tw, cons
                               bool pair, int grid, cudaStream_t s) {
   auto k = pair ? grouped_fp8_gemm_kernel<BWD, EPI, 1> : grouped_fp8_gemm_kernel<BWD, EPI, 0>;
   const size_t smem = smem_bytes8(p.E, pair);
-  cudaError_t err =
-      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // (always to the same value, so that calls from several host threads agree)
+  cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem_bytes8(1024, pair)));
   if (err != cudaSuccess) return err;
   if (!pair) return launch_pdl(k, dim3(grid), dim3(kThreads8), smem, s, ta, tw, p);
   cudaLaunchConfig_t cfg = {};
@@ -886,7 +887,9 @@ cudaError_t launch_fp8_gemm_t(const CUtensorMap& ta, const CUtensorMap& tw, cons
   int n = max_pairs[dev].load(std::memory_order_relaxed);
   if (n == 0) {
     cfg.numAttrs = 1;
+    cfg.dynamicSmemBytes = smem_bytes8(1024, 1);
     err = cudaOccupancyMaxActiveClusters(&n, k, &cfg);
+    cfg.dynamicSmemBytes = smem;
     if (err != cudaSuccess) return err;
     if (n < 1) return cudaErrorInvalidConfiguration;
     max_pairs[dev].store(n, std::memory_order_relaxed);

@@ -34,7 +34,7 @@ cudaError_t launch_route_scored(const float* logits, const float* bias, const vo
                                 int32_t* num_active, int32_t* chunk_offsets, int32_t* num_chunks,
                                 int32_t* perm_token, int32_t* inv_perm, void* x_perm,
                                 int32_t* block_counts, cudaStream_t s);
-cudaError_t launch_route_scored_bwd(const float* d_gates, const float* logits,
+cudaError_t launch_route_scored_bwd(const float* d_gates, const float* gates, const float* logits,
                                     const int32_t* topk_idx, int T, int E, int k,
                                     const moe_router& rt, float* d_logits, cudaStream_t s);
 // d_rows = gate * dy scattered to the slots, d_gates = dy . rows, in one pass.

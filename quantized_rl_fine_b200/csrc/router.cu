@@ -20,6 +20,7 @@ namespace {
 // 32 warps: two tokens each in large launches, one in small ones.
 constexpr int kScoredThreads = 1024;
 constexpr int kScoredWarps = kScoredThreads / 32;
+constexpr int kScoredMaxSmem = 200 * 1024;
 
 // False for NaN and -inf, which mask an expert.
 __device__ __forceinline__ bool is_open(float l) { return l > -INFINITY; }
@@ -222,7 +223,7 @@ __device__ __forceinline__ void select_token(const float* __restrict__ row, cons
     if (grouped) {
       float gap;
       const unsigned open = open_groups<float, NPER>(gv, reinterpret_cast<float*>(wrow), E, rt, lane, magic, &gap);
-      // a group score is one value or the sum of two
+      // (a group score is one value or the sum of two)
       if (scores) sure = gap > 2.0f * rt.group_top * err;
 #pragma unroll
       for (int i = 0; i < NPER; ++i) {
@@ -295,7 +296,7 @@ __device__ __forceinline__ void select_token(const float* __restrict__ row, cons
       }
     }
     if (bias && (close || odd)) {
-      if (odd || count == 32) {
+      if (odd || count == 32 || !(err < INFINITY)) {
         sure = false;
       } else if (sure) {
         // Order the candidates by their keys in 64 bits.
@@ -418,13 +419,14 @@ route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ 
   extern __shared__ double scored_sm[];   // [warps][row_el] group scratch; then [E] histogram
   grid_dependency_wait();
   grid_dependents_launch();
-  int32_t* hist = reinterpret_cast<int32_t*>(scored_sm + min(tpb, kScoredWarps) * row_el);
+  const int warps = blockDim.x >> 5;
+  int32_t* hist = reinterpret_cast<int32_t*>(scored_sm + warps * row_el);
   const bool with_hist = block_counts != nullptr;
   if (with_hist)
     for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int u = warp; u < tpb; u += kScoredWarps) {
+  for (int u = warp; u < tpb; u += warps) {
     const int t = blockIdx.x * tpb + u;
     if (t >= T) break;
     const float* row = logits + static_cast<int64_t>(t) * E;
@@ -503,8 +505,8 @@ route_scored_small_kernel(const float* __restrict__ logits, const float* __restr
 // FP32; the dense softmax part is in 32.
 constexpr int kBwdWarps = 8;
 __global__ void __launch_bounds__(kBwdWarps * 32)
-route_scored_bwd_kernel(const float* __restrict__ d_gates, const float* __restrict__ logits,
-                        const int32_t* __restrict__ topk_idx, int T, int E, int k, moe_router rt,
+route_scored_bwd_kernel(const float* __restrict__ d_gates, const float* __restrict__ gates,
+                        const float* __restrict__ logits, const int32_t* __restrict__ topk_idx, int T, int E, int k, moe_router rt,
                         float* __restrict__ d_logits) {
   extern __shared__ float bwd_sm[];     // [warps][E]
   grid_dependency_wait();
@@ -538,7 +540,8 @@ route_scored_bwd_kernel(const float* __restrict__ d_gates, const float* __restri
   double dw = 0.0, s = 0.0, rest = 0.0;   // rest: 1 - s of the sigmoid, without cancellation
   if (lane < k) {
     idx = __ldg(topk_idx + static_cast<int64_t>(t) * k + lane);
-    const float v = (idx >= 0 && idx < E) ? __ldg(row + idx) : -INFINITY;
+    float v = (idx >= 0 && idx < E) ? __ldg(row + idx) : -INFINITY;
+    if (gates && __ldg(gates + static_cast<int64_t>(t) * k + lane) == 0.0f) v = -INFINITY;   // masked in the forward
     if (is_open(v)) {
       dw = static_cast<double>(rt.scale) * __ldg(d_gates + static_cast<int64_t>(t) * k + lane);
       if (softmax) {
@@ -594,22 +597,24 @@ cudaError_t launch_route_scored(const float* logits, const float* bias, const vo
    : nper <= 8 ? CALL_(8)               \
    : nper <= 12 ? CALL_(12)             \
    : nper <= 16 ? CALL_(16) : CALL_(32))
-  auto go = [&](auto kern, int blocks, size_t sm, auto... args) {
-    if (sm > 40 * 1024) {
-      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(sm));
+  // (always to the same value, so that calls from several host threads agree)
+  auto go = [&](auto kern, int blocks, int threads, size_t sm, auto... args) {
+    if (sm > 32 * 1024) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoredMaxSmem);
       if (e != cudaSuccess) return e;
     }
-    return launch_pdl(kern, dim3(blocks), dim3(kScoredThreads), sm, s, args...);
+    return launch_pdl(kern, dim3(blocks), dim3(threads), sm, s, args...);
   };
   // one warp's group scratch, in doubles
   const int row_el = rt.groups > 1 ? group_pitch(E, rt.groups) * rt.groups : 0;
   const size_t row_sm = sizeof(double) * row_el;
-  // Few tokens: tokens of a block so that the scratch fits 200 KiB.
-  const int fit = row_sm == 0 ? kScoredWarps : static_cast<int>(std::min<size_t>(kScoredWarps, (200 * 1024) / row_sm));
+  // Warps of a block whose scratch fits (32, or 12 for the most padded groups).
+  const int fit = row_sm == 0 ? kScoredWarps
+                              : static_cast<int>(std::min<size_t>(kScoredWarps, (kScoredMaxSmem - 4096) / row_sm));
   if (T <= std::min(kSmallTokens, fit) && x == nullptr) {
 #define MOEQ_SMALL(N_)                                                                                             \
-  go(route_scored_small_kernel<N_>, 1, row_sm* T, logits, bias, T, E, k, row_el, rt, chunk_size, topk_idx, gates, \
+  go(route_scored_small_kernel<N_>, 1, kScoredThreads, row_sm* T, logits, bias, T, E, k, row_el, rt, chunk_size, topk_idx, gates, \
      offsets, active, num_active, chunk_offsets, num_chunks, perm_token, inv_perm)
     return MOEQ_BY_NPER(MOEQ_SMALL);
 #undef MOEQ_SMALL
@@ -619,9 +624,9 @@ cudaError_t launch_route_scored(const float* logits, const float* bias, const vo
   const int tpb = small ? fit : route_tokens_per_block();
   const int nblk = (T + tpb - 1) / tpb;
   int32_t* hist_out = small ? nullptr : block_counts;
-  const size_t sm = row_sm * std::min(tpb, kScoredWarps) + (small ? 0 : sizeof(int32_t) * E);
+  const size_t sm = row_sm * fit + (small ? 0 : sizeof(int32_t) * E);
 #define MOEQ_LARGE(N_) \
-  go(route_scored_kernel<N_>, nblk, sm, logits, bias, T, E, k, tpb, row_el, rt, topk_idx, gates, hist_out)
+  go(route_scored_kernel<N_>, nblk, 32 * fit, sm, logits, bias, T, E, k, tpb, row_el, rt, topk_idx, gates, hist_out)
   const cudaError_t err = MOEQ_BY_NPER(MOEQ_LARGE);
 #undef MOEQ_LARGE
 #undef MOEQ_BY_NPER
@@ -631,11 +636,11 @@ cudaError_t launch_route_scored(const float* logits, const float* bias, const vo
                              s);
 }
 
-cudaError_t launch_route_scored_bwd(const float* d_gates, const float* logits,
+cudaError_t launch_route_scored_bwd(const float* d_gates, const float* gates, const float* logits,
                                     const int32_t* topk_idx, int T, int E, int k,
                                     const moe_router& rt, float* d_logits, cudaStream_t s) {
   return launch_pdl(route_scored_bwd_kernel, dim3((T + kBwdWarps - 1) / kBwdWarps),
-                    dim3(kBwdWarps * 32), sizeof(float) * kBwdWarps * E, s, d_gates, logits, topk_idx,
+                    dim3(kBwdWarps * 32), sizeof(float) * kBwdWarps * E, s, d_gates, gates, logits, topk_idx,
                     T, E, k, rt, d_logits);
 }
 

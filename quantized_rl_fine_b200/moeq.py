@@ -104,7 +104,7 @@ def lib() -> ctypes.CDLL:
     gp = ctypes.POINTER(GroupsC)
     L.moe_route_scored.argtypes = [vp, vp, vp, i64, i32, i32, i64, rp, i32, vp, vp, vp, vp, vp, vp, vp,
                                    vp, vp, vp, vp, sz, vp]
-    L.moe_route_scored_bwd.argtypes = [vp, vp, vp, i64, i32, i32, rp, vp, vp]
+    L.moe_route_scored_bwd.argtypes = [vp, vp, vp, vp, i64, i32, i32, rp, vp, vp]
     L.moe_combine_bwd.argtypes = [vp, vp, vp, vp, i64, i32, i64, vp, vp, vp]
     L.moe_quantize_fp8_rows.argtypes = [vp, i64, i64, vp, i32, vp, vp, vp]
     L.moe_dequantize_fp8_rows.argtypes = [vp, vp, i64, i64, i32, vp, vp]
@@ -484,7 +484,8 @@ def moe_route_scored(logits: torch.Tensor, x: torch.Tensor | None, k: int, chunk
 
 def moe_route_scored_bwd(d_gates: torch.Tensor, logits: torch.Tensor, routing: Routing,
                          router: RouterSpec, stream=None, out: torch.Tensor | None = None) -> torch.Tensor:
-    """d_logits [T, E] from the gates' gradient [T, k] and the selection in `routing`."""
+    """d_logits [T, E] from the gates' gradient [T, k] and the selection (and gates, if kept) in
+    `routing`."""
     if logits.dim() != 2:
         raise ValueError("logits: expected [T, E]")
     T, E = logits.shape
@@ -492,14 +493,16 @@ def moe_route_scored_bwd(d_gates: torch.Tensor, logits: torch.Tensor, routing: R
     _need(logits, "logits", torch.float32, (T, E))
     _need(d_gates, "d_gates", torch.float32, (T, k), dev)
     _need(routing.topk_idx, "routing.topk_idx", torch.int32, (T, k), dev)
+    if routing.gates is not None:
+        _need(routing.gates, "routing.gates", torch.float32, (T, k), dev)
     rc = router.c()
     with _on(dev, stream):
         if out is None:
             out = torch.empty((T, E), dtype=torch.float32, device=dev)
         else:
             _need(out, "out", torch.float32, (T, E), dev)
-        _check(lib().moe_route_scored_bwd(_p(d_gates), _p(logits), _p(routing.topk_idx), T, E, k,
-                                          ctypes.byref(rc), _p(out), _here(dev)), "moe_route_scored_bwd")
+        _check(lib().moe_route_scored_bwd(_p(d_gates), _p(routing.gates), _p(logits), _p(routing.topk_idx),
+                                          T, E, k, ctypes.byref(rc), _p(out), _here(dev)), "moe_route_scored_bwd")
     return out
 
 

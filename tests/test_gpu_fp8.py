@@ -146,10 +146,17 @@ COUNTS = {
 SHAPES = [(16, 16), (128, 256), (272, 144), (1040, 400), (640, 1392)]
 
 
+@pytest.fixture(params=["0", "1"], ids=["single", "pair"])
+def ctas(request, monkeypatch):
+    """Single CTAs, or pairs, which sizes of more than 512 rows an expert take by themselves."""
+    monkeypatch.setenv("MOEQ_F8PAIR", request.param)
+    return request.param
+
+
 @pytest.mark.parametrize("name", sorted(COUNTS))
 @pytest.mark.parametrize("K,N", SHAPES)
 @pytest.mark.parametrize("bwd", [False, True])
-def test_product(name, K, N, bwd):
+def test_product(name, K, N, bwd, ctas):
     g = torch.Generator().manual_seed(K + N)
     counts = COUNTS[name]
     r, off = _routing(counts)
@@ -181,7 +188,7 @@ def _check_quantized(rows, want, delta, block, M, width):
 
 @pytest.mark.parametrize("name", sorted(COUNTS))
 @pytest.mark.parametrize("K,f,save", [(16, 128, True), (400, 128, False), (272, 384, True), (1024, 256, True)])
-def test_swiglu_product_and_checkpoint(name, K, f, save):
+def test_swiglu_product_and_checkpoint(name, K, f, save, ctas):
     g = torch.Generator().manual_seed(K + f)
     counts = COUNTS[name]
     r, off = _routing(counts)
@@ -209,7 +216,7 @@ def test_swiglu_product_and_checkpoint(name, K, f, save):
 
 @pytest.mark.parametrize("name", sorted(COUNTS))
 @pytest.mark.parametrize("N,f", [(16, 128), (400, 384), (1040, 256)])
-def test_swiglu_backward_from_checkpoint(name, N, f):
+def test_swiglu_backward_from_checkpoint(name, N, f, ctas):
     g = torch.Generator().manual_seed(N + f)
     counts = COUNTS[name]
     r, off = _routing(counts)
@@ -232,8 +239,8 @@ def test_swiglu_backward_from_checkpoint(name, N, f):
     _check_quantized(got, want, lim + 2.0 ** -8 * (np.abs(want) + lim), 128, M, 2 * f)
 
 
-def test_rows_do_not_depend_on_the_batch():
-    """A row's bits are the same alone and among others (forward, SwiGLU, backward)."""
+def test_rows_do_not_depend_on_the_batch(ctas):
+    """A row's bits are the same alone and among others (plain and SwiGLU)."""
     g = torch.Generator().manual_seed(2)
     K, f = 400, 128
     a, _ = _rows(g, 300, K)
@@ -275,7 +282,7 @@ def test_nothing_past_the_rows_is_written_and_nan_stays_in_its_row():
     assert np.all(np.abs(got[8:M + 8] - want)[rest] <= lim[rest])
 
 
-def test_tables_that_do_not_fit_the_rows_are_an_error_and_launch_no_tile():
+def test_tables_that_do_not_fit_the_rows_are_an_error_and_launch_no_tile(ctas):
     g = torch.Generator().manual_seed(8)
     a, _ = _rows(g, 40, 128)
     w, _ = _weight(g, 2, 128, 128)
@@ -321,7 +328,7 @@ def test_offsets_past_32_bits():
     assert not z[:100].any()
 
 
-def test_captured_replayed_and_two_streams_at_once():
+def test_captured_replayed_and_two_streams_at_once(ctas):
     g = torch.Generator().manual_seed(6)
     K, f, M = 256, 128, 200
     r, off = _routing([90, 0, 110])
@@ -355,3 +362,131 @@ def test_captured_replayed_and_two_streams_at_once():
     for i in range(2):
         assert all(torch.equal(a, b) for a, b in zip(got[i], want[i]))
     assert moeq.moe_get_device_error() == 0
+
+
+def test_single_and_pair_give_the_same_bits(monkeypatch):
+    g = torch.Generator().manual_seed(9)
+    K, f = 640, 256
+    r, off = _routing([300, 0, 5, 513])
+    M = int(off[-1])
+    a, _ = _rows(g, M, K)
+    w, _ = _weight(g, 4, 2 * f, K)
+    res = []
+    for p in "01":
+        monkeypatch.setenv("MOEQ_F8PAIR", p)
+        h, s = moeq.moe_grouped_fp8_gemm_fwd(a, w, r, moeq.EPI_SWIGLU, save_gu=True)
+        res.append((moeq.moe_grouped_fp8_gemm_fwd(a, w, r), h.q.view(torch.uint8), h.scales, s.q.view(torch.uint8), s.scales))
+    assert all(torch.equal(x, y) for x, y in zip(*res))
+
+
+def test_infinities_and_nan_in_the_epilogues(ctas):
+    """An accumulator that overflows or is NaN makes NaN where it enters, and the rest of its block is
+    quantized as if it were not there."""
+    f, K, M = 128, 128, 3
+    r, off = _routing([M])
+    codes = np.zeros((M, K), np.uint8)
+    codes[:, 0] = 0x38                                            # 1.0
+    a = moeq.Fp8Rows(_fp8(codes), torch.ones((1, M), device=DEV))
+    wc = np.full((1, 2 * f, K), 0x38, np.uint8)
+    ws = torch.full((1, 2, 1), 1.0, device=DEV)
+    # row 1 overflows through its scale, row 2 is NaN in one code
+    a.scales[0, 1] = 3.0e38
+    codes[2, 5] = 0x7F
+    a.q = _fp8(codes)
+    wc[0, 7, 0] = 0x7E                                            # gate feature 7 of row 1: 448 * 3e38
+    w = moeq.Fp8WeightT(_fp8(wc), ws)
+    h, s = moeq.moe_grouped_fp8_gemm_fwd(a, w, r, moeq.EPI_SWIGLU, save_gu=True)
+    hv, sv = f64(moeq.moe_dequantize_fp8_rows(h)), f64(moeq.moe_dequantize_fp8_rows(s))
+    assert moeq.moe_get_device_error() == 0
+    assert np.isfinite(hv[0]).all() and np.isfinite(sv[0]).all() and np.all(sv[0, :7] == 1.0) and sv[0, 7] == 448.0
+    assert np.isnan(sv[2]).all() and np.isnan(hv[2]).all()
+    # row 1: gate 7 overflowed; its neighbours are 3e38 to half a step; h = silu(3e38) * 3e38 overflows everywhere
+    assert np.isnan(sv[1, 7]) and np.all(np.abs(np.delete(sv[1], 7) / 3.0e38 - 1) <= 2.0 ** -4) and np.isnan(hv[1]).all()
+    # backward: dh finite, a checkpoint with NaN and infinite-like scales in single groups
+    d = moeq.Fp8Rows(_fp8(np.full((M, 128), 0x38, np.uint8)), torch.ones((1, M), device=DEV))
+    wd = moeq.Fp8WeightT(_fp8(np.full((1, 128, f), 0x38, np.uint8)), torch.ones((1, 1, 1), device=DEV))
+    ck = np.full((M, 2 * f), 0x38, np.uint8)
+    ck[1, 3] = 0x7F
+    X = np.full((8, M), 127, np.uint8)
+    X[5, 2] = 254                                                 # u of features 32..63 of row 2: 2^127
+    got = moeq.moe_grouped_fp8_gemm_bwd_dx(d, wd, r, moeq.EPI_SWIGLU_BWD, saved=moeq.Fp8Rows(_fp8(ck), torch.from_numpy(X).to(DEV)))
+    v = f64(moeq.moe_dequantize_fp8_rows(got))
+    sg = 1 / (1 + np.exp(-1.0))
+    dg, du = 128 * sg * (2 - sg), 128 * sg
+    near = lambda x, y: np.all(np.abs(x / y - 1) <= 2.0 ** -4 + 2.0 ** -7)       # noqa: E731  e4m3 and BF16
+    assert near(v[0, :f], dg) and near(v[0, f:], du)
+    assert np.isnan(v[1, 3]) and np.isnan(v[1, f + 3]) and near(np.delete(v[1, :f], 3), dg) and near(np.delete(v[1, f:], 3), du)
+    assert np.isnan(v[2, 32:64]).all() and near(v[2, :32], dg) and near(v[2, 64:f], dg) and near(v[2, f:], du)
+
+
+def test_waits_that_run_out_are_reported_and_the_next_call_is_clean(ctas):
+    """With a budget of 200 cycles a wait of tens of microseconds runs out: the checkpoint warp waits that long
+    for its next tile (56 reduction blocks), and there are more tiles than CTAs."""
+    f, R, counts = 256, 7168, [9000, 11000]
+    g = torch.Generator(device=DEV).manual_seed(7)
+    r, off = _routing(counts)
+    M = int(off[-1])
+    codes = lambda *n: (torch.randint(0, 0x70, n, generator=g, device=DEV, dtype=torch.int16).to(torch.uint8)     # noqa: E731
+                        .view(torch.float8_e4m3fn))
+    a = moeq.Fp8Rows(codes(M, R), torch.ones((R // 128, M), device=DEV))
+    w = moeq.Fp8WeightT(codes(2, R, f), torch.full((2, R // 128, 2), 1e-3, device=DEV))
+    ck = moeq.Fp8Rows(codes(M, 2 * f), torch.full((2 * f // 32, M), 120, dtype=torch.uint8, device=DEV))
+
+    def run():
+        d = moeq.moe_grouped_fp8_gemm_bwd_dx(a, w, r, moeq.EPI_SWIGLU_BWD, saved=ck)
+        return d.q.view(torch.uint8), d.scales
+    want = [t.clone() for t in run()]
+    assert moeq.moe_get_device_error() == moeq.DEVERR_NONE
+    try:
+        moeq.moe_test_set_wait_budget(200)
+        run()
+        code = moeq.moe_get_device_error()
+    finally:
+        moeq.moe_test_set_wait_budget(0)
+    assert code == moeq.DEVERR_WAIT_TIMEOUT
+    assert all(torch.equal(x, y) for x, y in zip(run(), want)) and moeq.moe_get_device_error() == moeq.DEVERR_NONE
+
+
+def test_pairs_of_experts_of_many_rows():
+    """More than 512 rows an expert: the pair kernel by the library's own choice, ragged ends of its 256-row tiles."""
+    g = torch.Generator().manual_seed(3)
+    counts = [700, 512, 769, 513]
+    K, N = 272, 400
+    r, off = _routing(counts)
+    a, av = _rows(g, int(off[-1]), K)
+    w, wv = _weight(g, 4, N, K)
+    want, mag = O8.fp8_gemm(av, wv, off)
+    lim = (K + 8) * 2 * U * mag
+    assert np.all(np.abs(f64(moeq.moe_grouped_fp8_gemm_fwd(a, w, r)) - want) <= 2.0 ** -8 * (np.abs(want) + lim) + lim)
+    assert moeq.moe_get_device_error() == 0
+
+
+def test_refusals_of_wrong_rows_and_weights():
+    g = torch.Generator().manual_seed(1)
+    r, _ = _routing([4, 4])
+    a, _ = _rows(g, 8, 128)
+    w, _ = _weight(g, 2, 256, 128)
+    F = moeq.Fp8Rows
+    for bad in (F(a.q[:, :112], a.scales), F(a.q.view(torch.uint8), a.scales), F(a.q, a.scales.double()), F(a.q, a.scales[:, :7]),
+                F(a.q[:, ::2], a.scales), F(a.q[0], a.scales)):
+        with pytest.raises(ValueError):
+            moeq.moe_grouped_fp8_gemm_fwd(bad, w, r)
+    with pytest.raises(ValueError):
+        moeq.moe_grouped_fp8_gemm_fwd(a, moeq.Fp8WeightT(w.q, w.scales.transpose(1, 2)), r)
+    with pytest.raises(ValueError):
+        moeq.moe_grouped_fp8_gemm_fwd(a, moeq.Fp8WeightT(w.q[:1].contiguous(), w.scales[:1].contiguous()), r)     # tables of two experts
+    with pytest.raises(ValueError):
+        moeq.moe_grouped_fp8_gemm_fwd(a, w, r, save_gu=True)
+    with pytest.raises(moeq.MoeError):
+        moeq.moe_grouped_fp8_gemm_fwd(a, w, r, moeq.EPI_SWIGLU_BWD)
+    d, _ = _rows(g, 8, 256)
+    with pytest.raises(ValueError):
+        moeq.moe_grouped_fp8_gemm_bwd_dx(d, w, r, moeq.EPI_SWIGLU_BWD)
+    with pytest.raises(ValueError):
+        moeq.moe_grouped_fp8_gemm_bwd_dx(d, w, r, saved=a)
+    with pytest.raises(ValueError):
+        moeq.moe_quantize_fp8_rows(torch.zeros((4, 32), device=DEV))
+    with pytest.raises(moeq.MoeError):
+        moeq.moe_quantize_fp8_rows(torch.zeros((4, 24), dtype=torch.bfloat16, device=DEV))
+    with pytest.raises(ValueError):
+        moeq.moe_quantize_fp8_rows(torch.zeros((5, 32), dtype=torch.bfloat16, device=DEV), r)

@@ -263,3 +263,115 @@ def test_router_chain_captured_and_on_another_stream():
     got = chain(*sets[1], stream=side)
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want[1]))
+
+
+@pytest.mark.parametrize("E,groups", [(1024, 32), (992, 31), (62, 31), (64, 32), (1000, 8), (513, 27)])
+@pytest.mark.parametrize("T", [1, 29, 40, 1100])
+def test_many_groups(E, groups, T):
+    """Group scratch from a few bytes to more than a block holds for 32 warps; both table paths and the one-launch one."""
+    g = torch.Generator().manual_seed(E + T)
+    logits = torch.randn((T, E), generator=g)
+    bias = 0.1 * torch.randn(E, generator=g)
+    for gt, b in ((1, None), (2, bias)):
+        _check(logits, 4, _spec(score="sigmoid", groups=groups, topk_groups=5, group_top=gt), b)
+
+
+def test_infinite_and_huge_biases():
+    T, E, k = 40, 48, 5
+    g = torch.Generator().manual_seed(12)
+    logits = torch.randn((T, E), generator=g)
+    bias = 0.1 * torch.randn(E, generator=g)
+    bias[3] = float("inf")
+    for kw in (dict(), dict(groups=4, topk_groups=2, group_top=2)):
+        _check(logits, k, _spec(score="sigmoid", **kw), bias)
+        _check(logits, k, _spec(score="softmax", **kw), bias * 1e30)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_experts_masked_by_the_bias_get_no_gradient(score, renorm):
+    """A bias of -inf leaves fewer than k experts: the slots filled up have gate 0, and neither they nor
+    their scores enter the gradient."""
+    T, E, k = 30, 6, 4
+    g = torch.Generator().manual_seed(2)
+    logits = torch.randn((T, E), generator=g)
+    bias = torch.tensor([0.0, -float("inf"), 0.1, -float("inf"), -float("inf"), -0.2])
+    dg = torch.randn((T, k), generator=g)
+    spec = _spec(score=score, renorm=renorm)
+    r, topk = _check(logits, k, spec, bias)
+    assert np.all(f64(r.gates)[:, 3] == 0) and np.all(f64(r.gates)[:, :3] > 0)
+    got = f64(moeq.moe_route_scored_bwd(dg.to(DEV), logits.to(DEV), r, spec))
+    want = O8.route_scored_bwd(dg.numpy(), logits.numpy(), topk, score, renorm, 1.0, gates=f64(r.gates))
+    # scores at most 1, the sum of three of them at least 1e-3 here: 256 U of |dg| / 1e-3
+    assert np.abs(got - want).max() <= 256 * U * np.abs(dg.numpy()).sum(1).max() * (1e3 if renorm else 1)
+    r.gates = None                                     # without the gates the scores count
+    assert not np.allclose(f64(moeq.moe_route_scored_bwd(dg.to(DEV), logits.to(DEV), r, spec)), want, rtol=1e-3)
+
+
+def test_combine_bwd_skips_slots_that_are_no_rows():
+    T, E, k, D = 6, 8, 2, 64
+    g = torch.Generator().manual_seed(4)
+    r = moeq.moe_route_scored(torch.randn((T, E), generator=g).to(DEV), None, k, 8, _spec())
+    dy = torch.randn((T, D), generator=g).to(torch.bfloat16).to(DEV)
+    rows = torch.randn((T * k, D), generator=g).to(torch.bfloat16).to(DEV)
+    want, wg = moeq.moe_combine_bwd(dy, rows, r)
+    lost = r.inv_perm[5].item(), r.inv_perm[8].item()
+    r.inv_perm = r.inv_perm.clone()
+    r.inv_perm[5], r.inv_perm[8] = -1, T * k
+    out = torch.full((T * k, D), 7.0, dtype=torch.bfloat16, device=DEV)
+    got, gg = moeq.moe_combine_bwd(dy, rows, r, out=out)
+    keep = [p for p in range(T * k) if p not in lost]
+    assert torch.equal(got[keep], want[keep]) and bool((got[list(lost)] == 7.0).all())
+    wg = wg.clone().view(-1)
+    wg[5] = wg[8] = 0
+    assert torch.equal(gg.view(-1), wg)
+
+
+def test_calls_from_several_host_threads():
+    """Different sizes at once, each thread on a stream of its own."""
+    import threading
+    jobs = [(20, 384, 8), (3000, 256, 8), (700, 1024, 32), (1, 64, 4)]
+    g = torch.Generator().manual_seed(8)
+    data = [(torch.randn((T, E), generator=g).to(DEV), (0.1 * torch.randn(E, generator=g)).to(DEV),
+             _spec(score="sigmoid", groups=gr, topk_groups=2, group_top=2)) for T, E, gr in jobs]
+    want = [moeq.moe_route_scored(lg, None, 4, 8, sp, bias=b) for lg, b, sp in data]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        s = torch.cuda.Stream()
+        for _ in range(20):
+            r = moeq.moe_route_scored(data[i][0], None, 4, 8, data[i][2], bias=data[i][1], stream=s)
+            s.synchronize()
+            if not (torch.equal(r.topk_idx, want[i].topk_idx) and torch.equal(r.inv_perm, want[i].inv_perm)):
+                bad.append(i)
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(len(jobs))]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not bad
+
+
+def test_refusals_of_wrong_tensors():
+    lg = torch.zeros((4, 8), device=DEV)
+    spec = _spec()
+    bad = [dict(logits=lg.half()), dict(logits=lg.t()), dict(logits=lg[:, ::2]), dict(bias=torch.zeros(7, device=DEV)),
+           dict(bias=torch.zeros(8)), dict(x=torch.zeros((4, 16), device=DEV)), dict(x=torch.zeros((3, 16), device=DEV, dtype=torch.bfloat16))]
+    for kw in bad:
+        a = dict(logits=lg, x=None, bias=None)
+        a.update(kw)
+        with pytest.raises(ValueError):
+            moeq.moe_route_scored(a["logits"], a["x"], 2, 8, spec, bias=a["bias"])
+    with pytest.raises(moeq.MoeError):
+        moeq.moe_route_scored(lg, None, 9, 8, spec)
+    r = moeq.moe_route_scored(lg, None, 2, 8, spec)
+    with pytest.raises(ValueError):
+        moeq.moe_route_scored(torch.zeros((5, 8), device=DEV), None, 2, 8, spec, out=r)
+    with pytest.raises(ValueError):
+        moeq.moe_route_scored_bwd(torch.zeros((4, 3), device=DEV), lg, r, spec)
+    rows = torch.zeros((8, 16), dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(moeq.MoeError):
+        moeq.moe_combine_bwd(rows[:4], rows, r, out=rows)              # in place
+    with pytest.raises(ValueError):
+        moeq.moe_combine_bwd(rows[:3], rows, r)

@@ -133,12 +133,12 @@ def test_route_scored_refusals(L):
 
 
 def test_router_gradient_refusals(L):
-    def call(dg=P, lg=P, idx=P, T=4, E=8, k=2, out=P, **kw):
-        return L.moe_route_scored_bwd(dg, lg, idx, T, E, k, ctypes.byref(_router(**kw)), out, None)
+    def call(dg=P, lg=P, idx=P, T=4, E=8, k=2, out=P, g=None, **kw):
+        return L.moe_route_scored_bwd(dg, g, lg, idx, T, E, k, ctypes.byref(_router(**kw)), out, None)
     for kw in (dict(dg=None), dict(lg=None), dict(idx=None), dict(out=None), dict(T=0), dict(E=1025), dict(k=9),
                dict(k=0), dict(score=5), dict(renorm=-1), dict(scale=float("inf"))):
         assert call(**kw) == 1, kw
-    assert call(dg=P + 4) == 2 and call(out=P + 8) == 2 and call(T=1 << 31) == 3
+    assert call(dg=P + 4) == 2 and call(out=P + 8) == 2 and call(g=P + 4) == 2 and call(T=1 << 31) == 3
 
     def comb(dy=P, rows=0x900000, inv=P, g=P, T=4, k=2, D=64, dr=0xA00000, dg=P):
         return L.moe_combine_bwd(dy, rows, inv, g, T, k, D, dr, dg, None)
