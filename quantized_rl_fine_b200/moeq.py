@@ -342,7 +342,9 @@ def moe_ep_regroup(counts: torch.Tensor, rows: torch.Tensor, direction: int, chu
 #
 # These calls check dtype, shape, layout (contiguous) and device of every
 # tensor, run on the tensors' own device, and allocate their outputs and
-# workspaces on the stream they launch on.
+# workspaces on the stream they launch on. For small batches the host is the
+# bound (a launch takes 3 us of a call's 8 to 20), hence sizes passed to
+# torch.empty one by one (a tuple costs 0.8 us) and few Python objects.
 # --------------------------------------------------------------------------
 
 def _need(t, name: str, dtype, shape, device=None):
@@ -432,10 +434,10 @@ def _new_routing(T: int, E: int, k: int, d: int | None, dev) -> Routing:
     sizes, tables = _routing_sizes(T, E, k)
     pieces = torch.empty(sum(sizes), dtype=torch.int32, device=dev).split_with_sizes(sizes)
     idx, off, act, nact, chunk, nchunk, perm, inv = (pieces[i] for i in tables)
-    return Routing(topk_idx=idx.view(T, k), gates=torch.empty((T, k), dtype=torch.float32, device=dev),
+    return Routing(topk_idx=idx.view(T, k), gates=torch.empty(T, k, dtype=torch.float32, device=dev),
                    expert_offsets=off, active=act, num_active=nact, chunk_offsets=chunk,
                    num_chunks=nchunk, perm_token=perm, inv_perm=inv,
-                   x_perm=None if d is None else torch.empty((T * k, d), dtype=torch.bfloat16, device=dev),
+                   x_perm=None if d is None else torch.empty(T * k, d, dtype=torch.bfloat16, device=dev),
                    E=E, k=k)
 
 
@@ -498,7 +500,7 @@ def moe_route_scored_bwd(d_gates: torch.Tensor, logits: torch.Tensor, routing: R
     rc = router.c()
     with _on(dev, stream):
         if out is None:
-            out = torch.empty((T, E), dtype=torch.float32, device=dev)
+            out = torch.empty(T, E, dtype=torch.float32, device=dev)
         else:
             _need(out, "out", torch.float32, (T, E), dev)
         _check(lib().moe_route_scored_bwd(_p(d_gates), _p(routing.gates), _p(logits), _p(routing.topk_idx),
@@ -520,10 +522,10 @@ def moe_combine_bwd(dy: torch.Tensor, rows: torch.Tensor, routing: Routing, stre
         _need(routing.gates, "routing.gates", torch.float32, (T, k), dev)
     with _on(dev, stream):
         if out is None:
-            out = torch.empty((T * k, D), dtype=torch.bfloat16, device=dev)
+            out = torch.empty(T * k, D, dtype=torch.bfloat16, device=dev)
         else:
             _need(out, "out", torch.bfloat16, (T * k, D), dev)
-        d_gates = torch.empty((T, k), dtype=torch.float32, device=dev)
+        d_gates = torch.empty(T, k, dtype=torch.float32, device=dev)
         _check(lib().moe_combine_bwd(_p(dy), _p(rows), _p(routing.inv_perm), _p(routing.gates), T, k, D,
                                      _p(out), _p(d_gates), _here(dev)), "moe_combine_bwd")
     return out, d_gates
@@ -578,23 +580,28 @@ def _need_fp8_rows(r: Fp8Rows, name: str, M: int, K: int, device, e8m0: bool = F
 
 
 def _new_fp8_rows(M: int, K: int, device, e8m0: bool = False) -> Fp8Rows:
-    scales = (torch.empty((-(-K // 32), M), dtype=torch.uint8, device=device) if e8m0 else
-              torch.empty((-(-K // 128), M), dtype=torch.float32, device=device))
-    return Fp8Rows(torch.empty((M, K), dtype=torch.float8_e4m3fn, device=device), scales)
+    scales = (torch.empty(-(-K // 32), M, dtype=torch.uint8, device=device) if e8m0 else
+              torch.empty(-(-K // 128), M, dtype=torch.float32, device=device))
+    return Fp8Rows(torch.empty(M, K, dtype=torch.float8_e4m3fn, device=device), scales)
 
 
 def _fp8_weight_c(w: Fp8WeightT, device) -> Fp8WeightC:
-    _need(w.q, "w.q", torch.float8_e4m3fn, w.q.shape, device)
-    if w.q.dim() != 3:
+    q = w.q
+    if q.dim() != 3:
         raise ValueError("w.q: expected [E, N, K]")
-    _need(w.scales, "w.scales", torch.float32, (w.E, -(-w.N // 128), -(-w.K // 128)), device)
-    return Fp8WeightC(_p(w.q), _p(w.scales), w.E, w.N, w.K)
+    E, N, K = q.shape
+    _need(q, "w.q", torch.float8_e4m3fn, (E, N, K), device)
+    _need(w.scales, "w.scales", torch.float32, (E, -(-N // 128), -(-K // 128)), device)
+    return Fp8WeightC(q.data_ptr(), w.scales.data_ptr(), E, N, K)
 
 
-def _groups_c(routing: Routing, w: Fp8WeightT, device) -> GroupsC:
-    for name, n in (("expert_offsets", w.E + 1), ("active", w.E), ("num_active", 1)):
-        _need(getattr(routing, name), "routing." + name, torch.int32, (n,), device)
-    return routing.groups()
+def _groups_c(routing: Routing, E: int, device) -> GroupsC:
+    i32 = torch.int32
+    _need(routing.expert_offsets, "routing.expert_offsets", i32, (E + 1,), device)
+    _need(routing.active, "routing.active", i32, (E,), device)
+    _need(routing.num_active, "routing.num_active", i32, (1,), device)
+    return GroupsC(routing.expert_offsets.data_ptr(), routing.active.data_ptr(),
+                   routing.num_active.data_ptr(), None, None, E)
 
 
 def moe_quantize_fp8_rows(x: torch.Tensor, routing: Routing | None = None, stream=None,
@@ -629,7 +636,7 @@ def moe_dequantize_fp8_rows(rows: Fp8Rows, stream=None, out: torch.Tensor | None
     _need_fp8_rows(rows, "rows", M, K, dev, rows.fmt == FP8_BLOCK32_E8M0)
     with _on(dev, stream):
         if out is None:
-            out = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+            out = torch.empty(M, K, dtype=torch.bfloat16, device=dev)
         else:
             _need(out, "out", torch.bfloat16, (M, K), dev)
         _check(lib().moe_dequantize_fp8_rows(_p(rows.q), _p(rows.scales), M, K, rows.fmt, _p(out),
@@ -644,18 +651,19 @@ def moe_grouped_fp8_gemm_fwd(a: Fp8Rows, w: Fp8WeightT, routing: Routing, epi: i
     if a.q.dim() != 2:
         raise ValueError("a.q: expected [M, K]")
     M, dev = a.q.shape[0], a.q.device
-    wc, g = _fp8_weight_c(w, dev), _groups_c(routing, w, dev)
-    _need_fp8_rows(a, "a", M, w.K, dev)
+    wc = _fp8_weight_c(w, dev)
+    g, N = _groups_c(routing, wc.E, dev), wc.N
+    _need_fp8_rows(a, "a", M, wc.K, dev)
     if save_gu and epi != EPI_SWIGLU:
         raise ValueError("save_gu: only with EPI_SWIGLU")
     with _on(dev, stream):
         if epi == EPI_SWIGLU:
-            h = _new_fp8_rows(M, w.N // 2, dev)
-            saved = _new_fp8_rows(M, w.N, dev, e8m0=True) if save_gu else None
+            h = _new_fp8_rows(M, N // 2, dev)
+            saved = _new_fp8_rows(M, N, dev, e8m0=True) if save_gu else None
             outs = (_p(h.q), _p(h.scales), _p(saved.q) if save_gu else None,
                     _p(saved.scales) if save_gu else None)
         else:
-            out = torch.empty((M, w.N), dtype=torch.bfloat16, device=dev)
+            out = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
             outs = (_p(out), None, None, None)
         _check(lib().moe_grouped_fp8_gemm_fwd(_p(a.q), _p(a.scales), M, ctypes.byref(wc), ctypes.byref(g),
                                               epi, *outs, _here(dev)), "moe_grouped_fp8_gemm_fwd")
@@ -669,19 +677,20 @@ def moe_grouped_fp8_gemm_bwd_dx(dout: Fp8Rows, w: Fp8WeightT, routing: Routing, 
     if dout.q.dim() != 2:
         raise ValueError("dout.q: expected [M, N]")
     M, dev = dout.q.shape[0], dout.q.device
-    wc, g = _fp8_weight_c(w, dev), _groups_c(routing, w, dev)
-    _need_fp8_rows(dout, "dout", M, w.N, dev)
+    wc = _fp8_weight_c(w, dev)
+    g, K = _groups_c(routing, wc.E, dev), wc.K
+    _need_fp8_rows(dout, "dout", M, wc.N, dev)
     glu = epi == EPI_SWIGLU_BWD
     if glu != (saved is not None):
         raise ValueError("saved: exactly with EPI_SWIGLU_BWD")
     if glu:
-        _need_fp8_rows(saved, "saved", M, 2 * w.K, dev, e8m0=True)
+        _need_fp8_rows(saved, "saved", M, 2 * K, dev, e8m0=True)
     with _on(dev, stream):
         if glu:
-            out = _new_fp8_rows(M, 2 * w.K, dev)
+            out = _new_fp8_rows(M, 2 * K, dev)
             outs = (_p(saved.q), _p(saved.scales), _p(out.q), _p(out.scales))
         else:
-            out = torch.empty((M, w.K), dtype=torch.bfloat16, device=dev)
+            out = torch.empty(M, K, dtype=torch.bfloat16, device=dev)
             outs = (None, None, _p(out), None)
         _check(lib().moe_grouped_fp8_gemm_bwd_dx(_p(dout.q), _p(dout.scales), M, ctypes.byref(wc),
                                                  ctypes.byref(g), epi, *outs, _here(dev)),
