@@ -523,9 +523,20 @@ moe_status run_fp8_gemm(bool bwd, int epi, const void* rows, const float* row_sc
   // the weight stream is the bound, which single CTAs feed better. Measured
   // (48 experts, K = 7168, N = 4096; single / pair, us): 100 rows 299 / 410,
   // 300 rows 787 / 912, 512 rows 990 / 1107, 700 rows 1387 / 1295, 768 rows
-  // 1494 / 1278. MOEQ_F8PAIR=0/1 overrides (tuning).
-  bool pair = M > 512 * static_cast<int64_t>(w->E);
-  if (const char* env = getenv("MOEQ_F8PAIR")) pair = atoi(env) == 1;
+  // 1494 / 1278.
+  // Tiles of 32 rows up to a mean of 16 rows an expert: a stage then holds little
+  // but weights, and five stages instead of three cover the latency of the
+  // stream; an expert of more than 32 rows costs a second tile. Measured (same
+  // weights, random routing; 128 / 32 rows a tile, us): 1 token of 8 experts
+  // 60 / 43, 2 tokens 110 / 79, 16 tokens 235 / 219, 16 rows an expert 279 / 247,
+  // 24 rows 290 / 265, 32 rows 290 / 350.
+  // MOEQ_F8FORM=0/1/2 (single, pair, few rows) overrides (tuning).
+  int form = M > 512 * static_cast<int64_t>(w->E) ? 1 : (M <= 16 * static_cast<int64_t>(w->E) ? 2 : 0);
+  if (const char* env = getenv("MOEQ_F8FORM")) {
+    const int v = atoi(env);
+    if (v >= 0 && v <= 2) form = v;
+  }
+  const bool pair = form == 1;
   // Rows and weights as boxes of 128 bytes x 128 rows, 128-byte swizzle; what
   // lies past the reduction length, the features or the rows reads as zeros.
   const uint64_t N = w->N, K = w->K, E = w->E, rl = R;
@@ -534,7 +545,8 @@ moe_status run_fp8_gemm(bool bwd, int epi, const void* rows, const float* row_sc
   const uint64_t wd[3] = {K, N, E};
   const uint64_t wst[2] = {K, N * K};
   const uint32_t box[3] = {128, 128, 1};
-  if (!make_map_3d(&ta, rows, CU_TENSOR_MAP_DATA_TYPE_UINT8, ad, as, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+  const uint32_t rbox[3] = {128, form == 2 ? 32u : 128u, 1};
+  if (!make_map_3d(&ta, rows, CU_TENSOR_MAP_DATA_TYPE_UINT8, ad, as, rbox, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map_3d(&tw, w->q, CU_TENSOR_MAP_DATA_TYPE_UINT8, wd, wst, box, CU_TENSOR_MAP_SWIZZLE_128B))
     return MOE_ERR_CUDA;
   Fp8GemmArgs p;
@@ -557,12 +569,12 @@ moe_status run_fp8_gemm(bool bwd, int epi, const void* rows, const float* row_sc
   p.saved = static_cast<uint8_t*>(saved);
   p.saved_scales = static_cast<uint8_t*>(saved_scales);
   // the most tiles that M rows over E experts can make; the list is 32-bit
-  const int64_t bound = static_cast<int64_t>(p.n_ftiles) * (std::min<int64_t>(w->E, M) + M / 128 + 1);
+  const int64_t bound = static_cast<int64_t>(p.n_ftiles) * (std::min<int64_t>(w->E, M) + M / (form == 2 ? 32 : 128) + 1);
   if (bound >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
   int64_t ctas = std::min<int64_t>(num_sms(), bound);
   if (pair) ctas = std::max<int64_t>(2, std::min<int64_t>(num_sms(), 2 * bound) / 2 * 2);
   return cuda_status(
-      launch_grouped_fp8_gemm(bwd, epi, ta, tw, p, pair, static_cast<int>(ctas), s));
+      launch_grouped_fp8_gemm(bwd, epi, ta, tw, p, form, static_cast<int>(ctas), s));
 }
 
 // Checks shared by the two FP8 products.

@@ -36,9 +36,20 @@ namespace {
 
 constexpr int kRows8 = 128;              // token rows per tile (MMA M)
 constexpr uint32_t kBoxBytes = 16384;    // one operand box: 128 rows x 128 bytes
-// One stage: the CTA's token rows and two weight boxes (one in a pair).
-__host__ __device__ constexpr uint32_t stage_bytes8(int pair) { return (pair ? 2u : 3u) * kBoxBytes; }
-__host__ __device__ constexpr int stages8(int pair) { return pair ? 4 : 3; }
+// Three forms: single CTAs on 128 token rows, pairs on 256, and single CTAs on
+// 32 rows for experts of few rows.
+constexpr int kSingle8 = 0, kPair8 = 1, kFew8 = 2;
+__host__ __device__ constexpr int tile_rows8(int form) { return form == kPair8 ? 256 : form == kFew8 ? 32 : 128; }
+// One stage: the CTA's token rows and two weight boxes (one in a pair). The MMA
+// always reads 128 rows of A; with 32 rows loaded the others are the weight
+// boxes behind them, and their products are not looked at.
+__host__ __device__ constexpr uint32_t row_bytes8(int form) { return form == kFew8 ? 4096u : kBoxBytes; }
+__host__ __device__ constexpr uint32_t stage_bytes8(int form) {
+  return row_bytes8(form) + (form == kPair8 ? 1u : 2u) * kBoxBytes;
+}
+__host__ __device__ constexpr int stages8(int form) { return form == kFew8 ? 5 : form == kPair8 ? 4 : 3; }
+// Lane quarters with rows, hence epilogue warps and staging slots in use.
+__host__ __device__ constexpr int quarters8(int form) { return form == kFew8 ? 1 : 4; }
 constexpr int kEpiWarp8 = 4;             // warp 0 copies, warp 1 issues MMAs, warps 4-11 epilogue
 constexpr int kEpiWarps8 = 8;
 constexpr int kThreads8 = 32 * (kEpiWarp8 + kEpiWarps8);
@@ -50,11 +61,13 @@ static_assert(128 * kRegsCopy + 256 * kRegsEpi <= kThreads8 * 168, "register spl
 // Output staging of one epilogue thread: its 256 bytes of a row, padded so
 // that the 16-byte stores of eight neighbouring threads fall in distinct banks.
 constexpr uint32_t kSlot8 = 272;
-constexpr size_t smem_bytes8(int E, int pair) {
-  return 1024 + stages8(pair) * stage_bytes8(pair) + 256 * kSlot8 + 8 * (2 * stages8(pair) + 10) + 16 + 4 * 4 * kRows8 + 4 * 32 +
+__host__ __device__ constexpr uint32_t slots_bytes8(int form) { return 64u * quarters8(form) * kSlot8; }
+constexpr size_t smem_bytes8(int E, int form) {
+  return 1024 + stages8(form) * stage_bytes8(form) + slots_bytes8(form) + 8 * (2 * stages8(form) + 10) + 16 + 4 * 4 * kRows8 + 4 * 32 +
          4 * 2 * (static_cast<size_t>(E) + 1) + 2 * static_cast<size_t>(E);
 }
-static_assert(smem_bytes8(1024, 0) <= 227 * 1024 && smem_bytes8(1024, 1) <= 227 * 1024, "shared memory of the largest stack");
+static_assert(smem_bytes8(1024, 0) <= 227 * 1024 && smem_bytes8(1024, 1) <= 227 * 1024 &&
+                  smem_bytes8(1024, 2) <= 227 * 1024, "shared memory of the largest stack");
 
 // D[tmem] (+)= A[smem] * B[smem]^T, e4m3 in, FP32 accumulation, K = 32.
 __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
@@ -142,9 +155,9 @@ struct Tile8 {
 // Tile t (a0: active index of an earlier tile): feature tile major, token tile
 // minor inside an expert, experts in active order, so the tiles in flight
 // share weights first.
-template <int PAIR>
+template <int FORM>
 __device__ __forceinline__ Tile8 tile8_at(const TileList8& tl, int t, int a0, int rank) {
-  constexpr int kTileRows = kRows8 << PAIR;
+  constexpr int kTileRows = tile_rows8(FORM);
   int lo = a0, hi = tl.A - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -158,16 +171,16 @@ __device__ __forceinline__ Tile8 tile8_at(const TileList8& tl, int t, int a0, in
   const int local = t - tl.start[lo];
   r.ft = local / nrt;
   r.row0 = seg0 + (local - r.ft * nrt) * kTileRows + rank * kRows8;
-  r.row_end = min(seg1, r.row0 + kRows8);
+  r.row_end = min(seg1, r.row0 + min(kTileRows, kRows8));
   return r;
 }
 
 // Builds the list; the active experts' rows must lie behind one another from
 // 0 to M. Tables that do not say so (or name an expert outside the stack) give
 // an empty list and the device error.
-template <int PAIR>
+template <int FORM>
 __device__ void build_tiles8(const Fp8GemmArgs& p, TileList8& tl, int32_t* warp_tot) {
-  constexpr int kTileRows = kRows8 << PAIR;
+  constexpr int kTileRows = tile_rows8(FORM);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, nw = blockDim.x >> 5;
   const int A_raw = *p.num_active;
   bool bad = !(A_raw >= 1 && A_raw <= p.E && p.offsets[0] == 0 && p.offsets[p.E] == p.M);
@@ -336,22 +349,25 @@ __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-template <int BWD, int EPI, int PAIR>
+template <int BWD, int EPI, int FORM>
 __global__ void __launch_bounds__(kThreads8, 1)
 grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
                         const __grid_constant__ CUtensorMap tm_w, const Fp8GemmArgs p) {
+  constexpr int PAIR = FORM == kPair8 ? 1 : 0;
+  constexpr int kQuarters = quarters8(FORM);
+  constexpr int kActive = 2 * kQuarters;         // epilogue warps with rows
   constexpr bool kGlu = !BWD && EPI == MOE_EPI_SWIGLU;
   constexpr bool kGluBwd = BWD && EPI == MOE_EPI_SWIGLU_BWD;
   extern __shared__ uint8_t smem_raw8[];
   const uint32_t raw = smem_u32(smem_raw8);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw8 + (base - raw);
-  constexpr int S = stages8(PAIR);
-  constexpr uint32_t kStage8 = stage_bytes8(PAIR);
+  constexpr int S = stages8(FORM);
+  constexpr uint32_t kStage8 = stage_bytes8(FORM);
   auto A_at = [&](int s) { return base + s * kStage8; };
-  auto B_at = [&](int s) { return base + s * kStage8 + kBoxBytes; };
+  auto B_at = [&](int s) { return base + s * kStage8 + row_bytes8(FORM); };
   const uint32_t stg_base = base + S * kStage8;
-  const uint32_t bars = stg_base + 256 * kSlot8;
+  const uint32_t bars = stg_base + slots_bytes8(FORM);
   auto full = [&](int s) { return bars + 8u * s; };
   auto empty = [&](int s) { return bars + 8u * (S + s); };
   auto acc_full = [&](int b) { return bars + 8u * (2 * S + b); };      // accumulator buffer b (two)
@@ -383,13 +399,13 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full(b), 2);               // the MMAs' commit and the scale warp
-      mbar_init(acc_empty(b), kEpiWarps8 << PAIR);
-      mbar_init(sc_free(b), kEpiWarps8);
+      mbar_init(acc_empty(b), kActive << PAIR);
+      mbar_init(sc_free(b), kActive);
     }
     mbar_init(drain_bar, 1);
-    mbar_init(amax_bar, kEpiWarps8);
+    mbar_init(amax_bar, kActive);
     mbar_init(gu_bar, 32);
-    mbar_init(slot_free, kEpiWarps8);
+    mbar_init(slot_free, kActive);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tm_a);
@@ -407,7 +423,7 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
   grid_dependency_wait();
   grid_dependents_launch();
 
-  build_tiles8<PAIR>(p, list, warp_tot);
+  build_tiles8<FORM>(p, list, warp_tot);
   const int total = list.start[list.A];
   const int nkb = p.nkb;                  // blocks of the reduction
   const int f_half = p.N >> 1;            // SwiGLU: first up row
@@ -430,7 +446,7 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
       Tile8 tl;
       tl.a = 0;
       for (int t = t_first; t < total && ok; t += t_step) {
-        tl = tile8_at<PAIR>(list, t, tl.a, rank);
+        tl = tile8_at<FORM>(list, t, tl.a, rank);
         const int c0 = kGlu ? tl.ft * 128 : tl.ft * 256;       // features of the two boxes
         const int c1 = kGlu ? f_half + tl.ft * 128 : c0 + 128;
         for (int kb = 0; kb < nkb; ++kb) {
@@ -515,7 +531,7 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
     Tile8 tl;
     tl.a = 0;
     for (int t = t_first; t < total && ok; t += t_step) {
-      tl = tile8_at<PAIR>(list, t, tl.a, rank);
+      tl = tile8_at<FORM>(list, t, tl.a, rank);
       // Blocks past the last feature (a tile that ends early) are clamped;
       // their columns are not stored.
       const float* pw = p.w_scales + static_cast<int64_t>(tl.e) * p.NB * p.KB;
@@ -531,15 +547,15 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
         up = static_cast<int64_t>(min(tl.ft * 2 + 1, p.NB - 1) - tl.ft * 2) * p.KB;
       }
       const float* pa = p.a_scales;
-      int off[4];
+      int off[kQuarters];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) off[i] = min(tl.row0 + 32 * i + lane, p.M - 1);
+      for (int i = 0; i < kQuarters; ++i) off[i] = min(tl.row0 + 32 * i + lane, p.M - 1);
       struct Set {
-        float a[4], w0, w1;
+        float a[kQuarters], w0, w1;
       } set[2];
       auto fetch = [&](Set& x) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x.a[i] = __ldg(pa + off[i]);
+        for (int i = 0; i < kQuarters; ++i) x.a[i] = __ldg(pa + off[i]);
         x.w0 = __ldg(pw);
         x.w1 = __ldg(pw + up);
         pa += p.M;
@@ -551,12 +567,13 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kActive; ++i) {
           const uint32_t pad = stg_base + static_cast<uint32_t>(i * 32 + lane) * kSlot8 + 256u;
+          const float sa = x.a[i % kQuarters];
           if constexpr (kGlu)
-            sts64(pad + 8u * b, __float_as_uint(x.a[i & 3] * x.w0), __float_as_uint(x.a[i & 3] * x.w1));
+            sts64(pad + 8u * b, __float_as_uint(sa * x.w0), __float_as_uint(sa * x.w1));
           else
-            sts32(pad + (kGluBwd ? 8u : 0u) + 4u * b, __float_as_uint(x.a[i & 3] * (i < 4 ? x.w0 : x.w1)));
+            sts32(pad + (kGluBwd ? 8u : 0u) + 4u * b, __float_as_uint(sa * (i < kQuarters ? x.w0 : x.w1)));
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_full(b));
@@ -572,21 +589,21 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
     }
   } else if (kGluBwd && warp == 3) {
     // ------------------------------------------------------------ checkpoint rows
-    // For the 256 staging slots (row, half) of each tile: the row's 128 bytes
+    // For the staging slots (half, row) of each tile: the row's 128 bytes
     // of g and of u by bulk copy, and its four plus four E8M0 scales.
     bool ok = true, any = false;
     int li = 0;
     Tile8 tl;
     tl.a = 0;
     for (int t = t_first; t < total; t += t_step, ++li) {
-      tl = tile8_at<PAIR>(list, t, tl.a, rank);
+      tl = tile8_at<FORM>(list, t, tl.a, rank);
       ok = mbar_wait8(slot_free, static_cast<uint32_t>(li & 1), abort_at);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       uint32_t valid = 0;
 #pragma unroll 1
-      for (int i = 0; i < 8; ++i) {
-        const int row = tl.row0 + (i & 3) * 32 + lane, f0 = tl.ft * 256 + (i >> 2) * 128;
+      for (int i = 0; i < kActive; ++i) {
+        const int row = tl.row0 + (i % kQuarters) * 32 + lane, f0 = tl.ft * 256 + (i / kQuarters) * 128;
         if (row >= tl.row_end || f0 >= p.K) continue;
         ++valid;
         const uint8_t* sc = p.saved_scales + static_cast<int64_t>(f0 / 32) * p.M + row;
@@ -601,8 +618,8 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
       mbar_arrive_expect_tx(gu_bar, 256 * valid);
       any = true;
 #pragma unroll 1
-      for (int i = 0; i < 8; ++i) {
-        const int row = tl.row0 + (i & 3) * 32 + lane, f0 = tl.ft * 256 + (i >> 2) * 128;
+      for (int i = 0; i < kActive; ++i) {
+        const int row = tl.row0 + (i % kQuarters) * 32 + lane, f0 = tl.ft * 256 + (i / kQuarters) * 128;
         if (row >= tl.row_end || f0 >= p.K) continue;
         const uint8_t* src = p.saved + static_cast<int64_t>(row) * (2 * p.K) + f0;
         const uint32_t dst = stg_base + static_cast<uint32_t>(i * 32 + lane) * kSlot8;
@@ -621,7 +638,7 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
     const int wg = (warp - kEpiWarp8) >> 2;      // column half
     const int r_in = q * 32 + lane;              // row of the tile
     const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-    const uint32_t slot = stg_base + static_cast<uint32_t>(threadIdx.x - 32 * kEpiWarp8) * kSlot8;
+    const uint32_t slot = stg_base + static_cast<uint32_t>(wg * 32 * kQuarters + r_in) * kSlot8;
     // This thread's 128 columns in two halves of 64: plain, one box; SwiGLU,
     // 64 gate columns and the 64 matching up columns.
     const uint32_t col0 = static_cast<uint32_t>(kGlu ? wg * 64 : wg * 128);
@@ -631,7 +648,7 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
     // here: the tile is kept as (row or -1, ft, a).
     int row = -1, ft = 0, ta = 0;
     auto enter = [&](int t) {
-      const Tile8 tl = tile8_at<PAIR>(list, t, ta, rank);
+      const Tile8 tl = tile8_at<FORM>(list, t, ta, rank);
       ta = tl.a;
       ft = tl.ft;
       row = tl.row0 + r_in;
@@ -639,8 +656,10 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
     };
     uint32_t it = 0;                             // reduction blocks so far (buffer it % 2)
     uint32_t li = 0;                             // parity of this CTA's tile count
-    if (t_first < total) enter(t_first);
-    for (int t = t_first; t < total; t += t_step, li ^= 1u) {
+    // (a warp whose lane quarter has no rows has nothing to do)
+    const int t_end = q < kQuarters ? total : 0;
+    if (t_first < t_end) enter(t_first);
+    for (int t = t_first; t < t_end; t += t_step, li ^= 1u) {
       const int cur_row = row, cur_ft = ft;
       uint64_t acc2[64];
 #pragma unroll
@@ -861,12 +880,15 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
 
 template <int BWD, int EPI>
 cudaError_t launch_fp8_gemm_t(const CUtensorMap& ta, const CUtensorMap& tw, const Fp8GemmArgs& p,
-                              bool pair, int grid, cudaStream_t s) {
-  auto k = pair ? grouped_fp8_gemm_kernel<BWD, EPI, 1> : grouped_fp8_gemm_kernel<BWD, EPI, 0>;
-  const size_t smem = smem_bytes8(p.E, pair);
+                              int form, int grid, cudaStream_t s) {
+  const bool pair = form == kPair8;
+  auto k = pair            ? grouped_fp8_gemm_kernel<BWD, EPI, kPair8>
+           : form == kFew8 ? grouped_fp8_gemm_kernel<BWD, EPI, kFew8>
+                           : grouped_fp8_gemm_kernel<BWD, EPI, kSingle8>;
+  const size_t smem = smem_bytes8(p.E, form);
   // (always to the same value, so that calls from several host threads agree)
   cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem_bytes8(1024, pair)));
+                                         static_cast<int>(smem_bytes8(1024, form)));
   if (err != cudaSuccess) return err;
   if (!pair) return launch_pdl(k, dim3(grid), dim3(kThreads8), smem, s, ta, tw, p);
   cudaLaunchConfig_t cfg = {};
@@ -906,12 +928,12 @@ cudaError_t launch_fp8_gemm_t(const CUtensorMap& ta, const CUtensorMap& tw, cons
 }  // namespace
 
 cudaError_t launch_grouped_fp8_gemm(bool bwd, int epi, const CUtensorMap& ta, const CUtensorMap& tw,
-                                    const Fp8GemmArgs& p, bool pair, int grid, cudaStream_t s) {
+                                    const Fp8GemmArgs& p, int form, int grid, cudaStream_t s) {
   if (!bwd)
-    return epi == MOE_EPI_SWIGLU ? launch_fp8_gemm_t<0, MOE_EPI_SWIGLU>(ta, tw, p, pair, grid, s)
-                                 : launch_fp8_gemm_t<0, MOE_EPI_NONE>(ta, tw, p, pair, grid, s);
-  return epi == MOE_EPI_SWIGLU_BWD ? launch_fp8_gemm_t<1, MOE_EPI_SWIGLU_BWD>(ta, tw, p, pair, grid, s)
-                                   : launch_fp8_gemm_t<1, MOE_EPI_NONE>(ta, tw, p, pair, grid, s);
+    return epi == MOE_EPI_SWIGLU ? launch_fp8_gemm_t<0, MOE_EPI_SWIGLU>(ta, tw, p, form, grid, s)
+                                 : launch_fp8_gemm_t<0, MOE_EPI_NONE>(ta, tw, p, form, grid, s);
+  return epi == MOE_EPI_SWIGLU_BWD ? launch_fp8_gemm_t<1, MOE_EPI_SWIGLU_BWD>(ta, tw, p, form, grid, s)
+                                   : launch_fp8_gemm_t<1, MOE_EPI_NONE>(ta, tw, p, form, grid, s);
 }
 
 }  // namespace moeq

@@ -24,8 +24,9 @@ struct Fp8GemmArgs {
   uint8_t* saved_scales;       // checkpoint E8M0 [2f/32][M]
 };
 
-// pair: clusters of two CTAs on 256 token rows (grid: CTAs, even).
+// form: 0 single CTAs on 128 token rows, 1 clusters of two CTAs on 256 (grid: CTAs,
+// even), 2 single CTAs on 32 token rows; the row map's box has 128 or (form 2) 32 rows.
 cudaError_t launch_grouped_fp8_gemm(bool bwd, int epi, const CUtensorMap& ta, const CUtensorMap& tw,
-                                    const Fp8GemmArgs& p, bool pair, int grid, cudaStream_t s);
+                                    const Fp8GemmArgs& p, int form, int grid, cudaStream_t s);
 
 }  // namespace moeq

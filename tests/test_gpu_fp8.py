@@ -146,10 +146,10 @@ COUNTS = {
 SHAPES = [(16, 16), (128, 256), (272, 144), (1040, 400), (640, 1392)]
 
 
-@pytest.fixture(params=["0", "1"], ids=["single", "pair"])
+@pytest.fixture(params=["0", "1", "2"], ids=["single", "pair", "few"])
 def ctas(request, monkeypatch):
-    """Single CTAs, or pairs, which sizes of more than 512 rows an expert take by themselves."""
-    monkeypatch.setenv("MOEQ_F8PAIR", request.param)
+    """Tiles of 128 rows, CTA pairs on 256 (by themselves from 512 rows an expert) and tiles of 32 (up to 16 rows)."""
+    monkeypatch.setenv("MOEQ_F8FORM", request.param)
     return request.param
 
 
@@ -364,7 +364,7 @@ def test_captured_replayed_and_two_streams_at_once(ctas):
     assert moeq.moe_get_device_error() == 0
 
 
-def test_single_and_pair_give_the_same_bits(monkeypatch):
+def test_all_forms_give_the_same_bits(monkeypatch):
     g = torch.Generator().manual_seed(9)
     K, f = 640, 256
     r, off = _routing([300, 0, 5, 513])
@@ -372,11 +372,11 @@ def test_single_and_pair_give_the_same_bits(monkeypatch):
     a, _ = _rows(g, M, K)
     w, _ = _weight(g, 4, 2 * f, K)
     res = []
-    for p in "01":
-        monkeypatch.setenv("MOEQ_F8PAIR", p)
+    for p in "012":
+        monkeypatch.setenv("MOEQ_F8FORM", p)
         h, s = moeq.moe_grouped_fp8_gemm_fwd(a, w, r, moeq.EPI_SWIGLU, save_gu=True)
         res.append((moeq.moe_grouped_fp8_gemm_fwd(a, w, r), h.q.view(torch.uint8), h.scales, s.q.view(torch.uint8), s.scales))
-    assert all(torch.equal(x, y) for x, y in zip(*res))
+    assert all(torch.equal(x, y) and torch.equal(x, z) for x, y, z in zip(*res))
 
 
 def test_infinities_and_nan_in_the_epilogues(ctas):

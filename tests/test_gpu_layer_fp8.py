@@ -48,7 +48,7 @@ def _wv(w):
                                                         (4, 2, 256, 128, 900, "sigmoid", True, "1"),
                                                         (16, 4, 128, 128, 1, "sigmoid", True, "0")])
 def test_fp8_layer_step(E, k, d, f, T, score, renorm, pair, monkeypatch):
-    monkeypatch.setenv("MOEQ_F8PAIR", pair)
+    monkeypatch.setenv("MOEQ_F8FORM", pair)
     g, x, dy, wg, wd = _fp8_layer(E, d, f, T, E + T)
     logits = torch.randn((T, E), generator=g).to(DEV)
     bias = (0.1 * torch.randn(E, generator=g)).to(DEV)
