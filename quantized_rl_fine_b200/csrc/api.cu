@@ -524,17 +524,20 @@ moe_status run_fp8_gemm(bool bwd, int epi, const void* rows, const float* row_sc
   // (48 experts, K = 7168, N = 4096; single / pair, us): 100 rows 299 / 410,
   // 300 rows 787 / 912, 512 rows 990 / 1107, 700 rows 1387 / 1295, 768 rows
   // 1494 / 1278.
-  // Tiles of 32 rows up to a mean of 16 rows an expert: a stage then holds little
-  // but weights, and five stages instead of three cover the latency of the
-  // stream; an expert of more than 32 rows costs a second tile. Measured (same
-  // weights, random routing; 128 / 32 rows a tile, us): 1 token of 8 experts
-  // 60 / 43, 2 tokens 110 / 79, 16 tokens 235 / 219, 16 rows an expert 279 / 247,
-  // 24 rows 290 / 265, 32 rows 290 / 350.
-  // MOEQ_F8FORM=0/1/2 (single, pair, few rows) overrides (tuning).
-  int form = M > 512 * static_cast<int64_t>(w->E) ? 1 : (M <= 16 * static_cast<int64_t>(w->E) ? 2 : 0);
+  // Tiles of 32 rows up to a mean of 16 rows an expert and of 64 up to 40: a
+  // stage then holds little but weights, and five or four stages instead of
+  // three cover the latency of the stream; an expert of more rows than a tile
+  // costs a second one. Measured (same weights, random routing; 128 / 64 / 32
+  // rows a tile, us): 1 token of 8 experts 60 / - / 43, 2 tokens 110 / - / 79,
+  // 16 rows an expert 270 / 258 / 248 (SwiGLU with checkpoint 292 / 269 / 267),
+  // 32 rows 287 / 266 / 312 (302 / 290 / 347), 48 rows 296 / 279 / 429
+  // (307 / 290 / 477), 64 rows 310 / 342 / 496.
+  // MOEQ_F8FORM=0/1/2/3 (128 rows, pair, 32 rows, 64 rows) overrides (tuning).
+  const int64_t e64 = w->E;
+  int form = M > 512 * e64 ? 1 : M <= 16 * e64 ? 2 : M <= 40 * e64 ? 3 : 0;
   if (const char* env = getenv("MOEQ_F8FORM")) {
     const int v = atoi(env);
-    if (v >= 0 && v <= 2) form = v;
+    if (v >= 0 && v <= 3) form = v;
   }
   const bool pair = form == 1;
   // Rows and weights as boxes of 128 bytes x 128 rows, 128-byte swizzle; what
@@ -545,7 +548,7 @@ moe_status run_fp8_gemm(bool bwd, int epi, const void* rows, const float* row_sc
   const uint64_t wd[3] = {K, N, E};
   const uint64_t wst[2] = {K, N * K};
   const uint32_t box[3] = {128, 128, 1};
-  const uint32_t rbox[3] = {128, form == 2 ? 32u : 128u, 1};
+  const uint32_t rbox[3] = {128, form == 2 ? 32u : form == 3 ? 64u : 128u, 1};
   if (!make_map_3d(&ta, rows, CU_TENSOR_MAP_DATA_TYPE_UINT8, ad, as, rbox, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map_3d(&tw, w->q, CU_TENSOR_MAP_DATA_TYPE_UINT8, wd, wst, box, CU_TENSOR_MAP_SWIZZLE_128B))
     return MOE_ERR_CUDA;
@@ -569,7 +572,7 @@ moe_status run_fp8_gemm(bool bwd, int epi, const void* rows, const float* row_sc
   p.saved = static_cast<uint8_t*>(saved);
   p.saved_scales = static_cast<uint8_t*>(saved_scales);
   // the most tiles that M rows over E experts can make; the list is 32-bit
-  const int64_t bound = static_cast<int64_t>(p.n_ftiles) * (std::min<int64_t>(w->E, M) + M / (form == 2 ? 32 : 128) + 1);
+  const int64_t bound = static_cast<int64_t>(p.n_ftiles) * (std::min<int64_t>(w->E, M) + M / std::min(128u, rbox[1]) + 1);
   if (bound >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
   int64_t ctas = std::min<int64_t>(num_sms(), bound);
   if (pair) ctas = std::max<int64_t>(2, std::min<int64_t>(num_sms(), 2 * bound) / 2 * 2);

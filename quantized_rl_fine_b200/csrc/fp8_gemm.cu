@@ -36,20 +36,20 @@ namespace {
 
 constexpr int kRows8 = 128;              // token rows per tile (MMA M)
 constexpr uint32_t kBoxBytes = 16384;    // one operand box: 128 rows x 128 bytes
-// Three forms: single CTAs on 128 token rows, pairs on 256, and single CTAs on
-// 32 rows for experts of few rows.
-constexpr int kSingle8 = 0, kPair8 = 1, kFew8 = 2;
-__host__ __device__ constexpr int tile_rows8(int form) { return form == kPair8 ? 256 : form == kFew8 ? 32 : 128; }
+// Four forms: single CTAs on 128 token rows, pairs on 256, and single CTAs on
+// 32 or 64 rows for experts of few rows.
+constexpr int kSingle8 = 0, kPair8 = 1, kFew8 = 2, kSome8 = 3;
+// Lane quarters with rows in one CTA, hence epilogue warps and staging slots in use.
+__host__ __device__ constexpr int quarters8(int form) { return form == kFew8 ? 1 : form == kSome8 ? 2 : 4; }
+__host__ __device__ constexpr int tile_rows8(int form) { return form == kPair8 ? 256 : 32 * quarters8(form); }
 // One stage: the CTA's token rows and two weight boxes (one in a pair). The MMA
-// always reads 128 rows of A; with 32 rows loaded the others are the weight
+// always reads 128 rows of A; with fewer loaded the others are the weight
 // boxes behind them, and their products are not looked at.
-__host__ __device__ constexpr uint32_t row_bytes8(int form) { return form == kFew8 ? 4096u : kBoxBytes; }
+__host__ __device__ constexpr uint32_t row_bytes8(int form) { return 4096u * quarters8(form); }
 __host__ __device__ constexpr uint32_t stage_bytes8(int form) {
   return row_bytes8(form) + (form == kPair8 ? 1u : 2u) * kBoxBytes;
 }
-__host__ __device__ constexpr int stages8(int form) { return form == kFew8 ? 5 : form == kPair8 ? 4 : 3; }
-// Lane quarters with rows, hence epilogue warps and staging slots in use.
-__host__ __device__ constexpr int quarters8(int form) { return form == kFew8 ? 1 : 4; }
+__host__ __device__ constexpr int stages8(int form) { return form == kSingle8 ? 3 : form == kFew8 ? 5 : 4; }
 constexpr int kEpiWarp8 = 4;             // warp 0 copies, warp 1 issues MMAs, warps 4-11 epilogue
 constexpr int kEpiWarps8 = 8;
 constexpr int kThreads8 = 32 * (kEpiWarp8 + kEpiWarps8);
@@ -67,7 +67,7 @@ constexpr size_t smem_bytes8(int E, int form) {
          4 * 2 * (static_cast<size_t>(E) + 1) + 2 * static_cast<size_t>(E);
 }
 static_assert(smem_bytes8(1024, 0) <= 227 * 1024 && smem_bytes8(1024, 1) <= 227 * 1024 &&
-                  smem_bytes8(1024, 2) <= 227 * 1024, "shared memory of the largest stack");
+                  smem_bytes8(1024, 2) <= 227 * 1024 && smem_bytes8(1024, 3) <= 227 * 1024, "shared memory of the largest stack");
 
 // D[tmem] (+)= A[smem] * B[smem]^T, e4m3 in, FP32 accumulation, K = 32.
 __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
@@ -884,6 +884,7 @@ cudaError_t launch_fp8_gemm_t(const CUtensorMap& ta, const CUtensorMap& tw, cons
   const bool pair = form == kPair8;
   auto k = pair            ? grouped_fp8_gemm_kernel<BWD, EPI, kPair8>
            : form == kFew8 ? grouped_fp8_gemm_kernel<BWD, EPI, kFew8>
+           : form == kSome8 ? grouped_fp8_gemm_kernel<BWD, EPI, kSome8>
                            : grouped_fp8_gemm_kernel<BWD, EPI, kSingle8>;
   const size_t smem = smem_bytes8(p.E, form);
   // (always to the same value, so that calls from several host threads agree)
