@@ -518,12 +518,13 @@ moe_status run_fp8_gemm(bool bwd, int epi, const void* rows, const float* row_sc
   const int tile_f = (!bwd && epi == MOE_EPI_SWIGLU) ? 128 : 256;
   CUtensorMap ta, tw;
   // CTA pairs (256-row tiles) once the mean expert holds more than 512 rows: a
-  // pair moves a third less weight through L2 and shared memory per product,
-  // but pads an expert's rows to 256 instead of 128, and below about 300 rows
-  // the weight stream is the bound, which single CTAs feed better. Measured
-  // (48 experts, K = 7168, N = 4096; single / pair, us): 100 rows 299 / 410,
-  // 300 rows 787 / 912, 512 rows 990 / 1107, 700 rows 1387 / 1295, 768 rows
-  // 1494 / 1278.
+  // pair moves a third less weight through L2 and shared memory per product and
+  // takes 0.86 of the time per padded row, but pads an expert's rows to 256
+  // instead of 128 (64 rows more on average, which 0.14 x 460 rows pay for).
+  // Measured (48 experts, K = 7168, N = 4096, random routing; single / pair, us):
+  // 100 rows 286 / 410, 300 rows 630 / 750, 512 rows 1010 / 965, 600 rows
+  // 1050 / 1150 (640 against 768 padded rows), 700 rows 1240 / 1075, 768 rows
+  // 1385 / 1370, 1000 rows 1640 / 1640; 768 rows in every expert: pair 1196.
   // Tiles of 32 rows up to a mean of 16 rows an expert and of 64 up to 40: a
   // stage then holds little but weights, and five or four stages instead of
   // three cover the latency of the stream; an expert of more rows than a tile

@@ -433,12 +433,13 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      // Single CTAs serve experts of few row tiles, whose weights are read once
-      // or twice in quick succession; pairs read them for three row tiles and
-      // more, and evict-first lost them in between (DRAM reads 1.5 times the
-      // algorithm's, 1257 us instead of 1196 at 768 rows x 48 experts).
+      // Weights of experts of one row tile are read once and make room first;
+      // where an expert has several they are read again, and evict-first lost
+      // them in between (pairs, 768 rows x 48 experts: DRAM reads 1.5 times the
+      // algorithm's, 1257 us instead of 1196; single CTAs, 300 rows: 690 -> 650).
+      constexpr bool kOnce = FORM == kFew8 || FORM == kSome8;
       const uint64_t pol_a = l2_policy_evict_last();
-      const uint64_t pol_w = PAIR ? l2_policy_evict_last() : l2_policy_evict_first();
+      const uint64_t pol_w = kOnce ? l2_policy_evict_first() : l2_policy_evict_last();
       int st = 0;
       uint32_t ph = 0;
       long long issued = 0;
