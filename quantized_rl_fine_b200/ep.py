@@ -104,6 +104,7 @@ def expert_compute(rows: torch.Tensor, recv_counts: torch.Tensor, w_gu: QWeightT
                    w_d: QWeightT | M.Fp8WeightT, chunk_size: int, adapter: torch.Tensor | None = None) -> torch.Tensor:
     """Phase 2 on the owner: received rows (source-major) -> local expert-major
     -> gate/up + SwiGLU -> down -> back to source-major order."""
+    layer.check_weights(w_gu, w_d)
     if rows.shape[0] == 0:                      # no token chose this rank's experts
         return rows.new_empty((0, w_d.N))
     xl, groups = M.moe_ep_regroup(recv_counts, rows, 0, chunk_size)

@@ -40,11 +40,17 @@ def route(logits: torch.Tensor, x: torch.Tensor | None, k: int, chunk_size: int,
     return M.moe_route_permute(logits, x, k, chunk_size, stream=stream)
 
 
+def check_weights(w_gu: QWeightT | M.Fp8WeightT, w_d: QWeightT | M.Fp8WeightT):
+    if isinstance(w_gu, M.Fp8WeightT) != isinstance(w_d, M.Fp8WeightT):
+        raise ValueError("w_gu and w_d: both 4-bit or both FP8 (the rows between them have one format)")
+
+
 def forward(x: torch.Tensor, logits: torch.Tensor, w_gu: QWeightT | M.Fp8WeightT,
             w_d: QWeightT | M.Fp8WeightT, k: int, chunk_size: int, adapter: torch.Tensor | None = None,
             train: bool = False, stream=None, gather: bool | None = None,
             router: M.RouterSpec | None = None, bias: torch.Tensor | None = None) -> dict:
     T = x.shape[0]
+    check_weights(w_gu, w_d)
     scored = dict(router=router, logits=logits if router is not None else None)
     if isinstance(w_gu, M.Fp8WeightT):
         if adapter is not None or gather:
@@ -71,6 +77,7 @@ def backward(state: dict, dy: torch.Tensor, w_gu: QWeightT | M.Fp8WeightT, w_d: 
     """Gradients of the step; with a router also d_gates [T, k] and d_logits [T, E]."""
     r: M.Routing = state["routing"]
     T = dy.shape[0]
+    check_weights(w_gu, w_d)
     d_gates = d_logits = None
     if state.get("router") is not None:
         dy_perm, d_gates = M.moe_combine_bwd(dy, state["y_perm"], r, stream=stream)

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from oracle import scored_fp8 as O8
-from quantized_rl_fine_b200 import accounting, build, layer, moeq, synth
+from quantized_rl_fine_b200 import accounting, build, ep, layer, moeq, synth
 
 
 # ----------------------------------------------------------------------------- definitions
@@ -195,3 +195,11 @@ def test_bindings_refuse_on_the_host():
         layer.route(lg, None, 2, 8, None, bias=torch.zeros(8))
     with pytest.raises(ValueError):
         layer.forward(lg, lg, w, w, 2, 8, adapter=torch.zeros(1))
+    four = synth.QWeightT("int4", torch.zeros((2, 64, 32), dtype=torch.uint8), torch.ones((2, 2, 64), dtype=torch.bfloat16))
+    for pair in ((w, four), (four, w)):                                 # one layer, one format
+        with pytest.raises(ValueError, match="both"):
+            layer.forward(lg, lg, *pair, 2, 8)
+        with pytest.raises(ValueError, match="both"):
+            layer.backward(dict(routing=None), lg, *pair)
+        with pytest.raises(ValueError, match="both"):
+            ep.expert_compute(lg, lg, *pair, 8)
