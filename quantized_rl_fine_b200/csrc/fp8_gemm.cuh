@@ -22,10 +22,11 @@ struct Fp8GemmArgs {
   float* out_scales;           // e4m3 rows: [blocks][M]
   uint8_t* saved;              // checkpoint e4m3 [M][2f]: written (forward, may be NULL) or read
   uint8_t* saved_scales;       // checkpoint E8M0 [2f/32][M]
+  int32_t w_once;              // 1: weights leave L2 first (an expert's are read once)
 };
 
 // form: 0 single CTAs on 128 token rows, 1 clusters of two CTAs on 256 (grid: CTAs,
-// even), 2 single CTAs on 32 token rows; the row map's box has 128 or (form 2) 32 rows.
+// even), 2 and 3 single CTAs on 32 and 64. The row map's box has 128, 128, 32, 64 rows.
 cudaError_t launch_grouped_fp8_gemm(bool bwd, int epi, const CUtensorMap& ta, const CUtensorMap& tw,
                                     const Fp8GemmArgs& p, int form, int grid, cudaStream_t s);
 

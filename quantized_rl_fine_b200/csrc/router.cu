@@ -7,7 +7,12 @@
 //
 // A token's selection is a chain of dependent warp reductions (about 2 us),
 // so what bounds it is latency: a warp per token, everything in registers,
-// three launches for many tokens and one for a decode batch.
+// three launches for many tokens and one for a decode batch. Measured, whole
+// call in a graph: 1 token of 384 experts in 8 groups with bias 8.7 us, 32
+// tokens 14.5, 4096 tokens of 256 experts 32.5 (about 13 of it the scan of the
+// counts and the scatter), 16384 of 384 softmax without groups 39.5 (to read
+// the 25 MB of logits would take 4). FP32 keys against 64-bit keys
+// throughout: 39.5 / 88 and 32.5 / 51 us.
 #include <algorithm>
 
 #include "common.cuh"
@@ -502,12 +507,13 @@ route_scored_small_kernel(const float* __restrict__ logits, const float* __restr
 // row of the warp's shared memory, then the whole row of d_logits written
 // once. What belongs to the k selected scores is in 64 bits, because renorm
 // subtracts nearly equal numbers and divides by a sum that may lie below
-// FP32; the dense softmax part is in 32.
+// FP32; the dense softmax part is in 32. Bound: DRAM, one row of logits read
+// (softmax) and one of d_logits written; 4096 x 384 takes 11 us, 6.3 MB written.
 constexpr int kBwdWarps = 8;
 __global__ void __launch_bounds__(kBwdWarps * 32)
 route_scored_bwd_kernel(const float* __restrict__ d_gates, const float* __restrict__ gates,
-                        const float* __restrict__ logits, const int32_t* __restrict__ topk_idx, int T, int E, int k, moe_router rt,
-                        float* __restrict__ d_logits) {
+                        const float* __restrict__ logits, const int32_t* __restrict__ topk_idx, int T, int E,
+                        int k, moe_router rt, float* __restrict__ d_logits) {
   extern __shared__ float bwd_sm[];     // [warps][E]
   grid_dependency_wait();
   grid_dependents_launch();

@@ -379,6 +379,23 @@ def test_all_forms_give_the_same_bits(monkeypatch):
     assert all(torch.equal(x, y) for z in res[1:] for x, y in zip(res[0], z))
 
 
+@pytest.mark.parametrize("M", [64, 65, 160, 161, 256, 257, 2048, 2049])
+def test_the_form_chosen_by_the_mean_rows_changes_no_bit(M, monkeypatch):
+    """Four experts: 16, 40, 64 and 512 mean rows and one more, most of them in one expert."""
+    g = torch.Generator().manual_seed(M)
+    K, N = 272, 400
+    r, off = _routing([1, M - 34, 0, 33])
+    a, _ = _rows(g, M, K)
+    d, _ = _rows(g, M, N)
+    w, _ = _weight(g, 4, N, K)
+    monkeypatch.delenv("MOEQ_F8FORM", raising=False)
+    got = (moeq.moe_grouped_fp8_gemm_fwd(a, w, r), moeq.moe_grouped_fp8_gemm_bwd_dx(d, w, r))
+    monkeypatch.setenv("MOEQ_F8FORM", "0")
+    want = (moeq.moe_grouped_fp8_gemm_fwd(a, w, r), moeq.moe_grouped_fp8_gemm_bwd_dx(d, w, r))
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert moeq.moe_get_device_error() == 0
+
+
 def test_infinities_and_nan_in_the_epilogues(ctas):
     """An accumulator that overflows or is NaN makes NaN where it enters, and the rest of its block is
     quantized as if it were not there."""
