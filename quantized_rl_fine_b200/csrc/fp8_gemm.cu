@@ -26,12 +26,12 @@
 // draining its pipeline counts); 62 rows x 64 experts of 2048 x 2048 57 us (5.3 TB/s).
 // Many rows: the hand-over between tensor core and epilogue. Per 128 x 256 x 128
 // block the MMAs alone take 565 cycles, with barriers but no tensor-memory
-// reads 768, complete about 1000: commit, wake-up, two rounds of
+// reads 768, complete about 970: commit, wake-up, two rounds of
 // tensor-memory loads and the release follow one another, and only two buffers
-// of 256 columns fit. 768 rows x 48 experts, K 7168, N 4096: 1060 us at full
-// clocks (2.04 PFLOP/s), 1196 under the power cap; backward 1080 / 1178;
-// SwiGLU with checkpoint 1105 / 1297 (its epilogue, about 5 us a tile, is not
-// overlapped: the accumulators are in registers). SwiGLU backward 620 us for
+// of 256 columns fit. 768 rows x 48 experts, K 7168, N 4096: 1037 us at full
+// clocks (2.09 PFLOP/s), 1190 under the power cap; backward 1074 / 1248; SwiGLU
+// 1060 / 1219, with checkpoint 1132 / 1312 (its epilogue, about 5 us a tile, is
+// not overlapped: the accumulators are in registers). SwiGLU backward 620 us for
 // half the work.
 // Tried, without gain: 128-column tiles or a column split with their own barriers
 // (the time per hand-over stays), two MMA issuers, spinning waits, tensor-memory

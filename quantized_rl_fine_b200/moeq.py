@@ -418,27 +418,26 @@ def _scored_ws_bytes(T: int, E: int, k: int, router: RouterSpec, chunk_size: int
 
 
 @functools.lru_cache(maxsize=256)
-def _routing_sizes(T: int, E: int, k: int) -> tuple[list[int], list[int]]:
-    """Split sizes of one int32 buffer into the eight tables (each starting on 16 bytes) and the
-    padding between them, and which of the pieces are tables."""
-    sizes, tables = [], []
-    for n in (T * k, E + 1, E, 1, E + 1, 1, T * k, T * k):
-        tables.append(len(sizes))
+def _routing_layout(T: int, E: int, k: int) -> tuple[list[int], list[int], list[int]]:
+    """Split sizes of one 32-bit buffer into the gates and the eight tables (each starting on 16
+    bytes) and the padding between them, which of the pieces are these nine, and their byte offsets."""
+    sizes, pieces, at = [], [], []
+    for n in (T * k, T * k, E + 1, E, 1, E + 1, 1, T * k, T * k):
+        pieces.append(len(sizes))
+        at.append(4 * sum(sizes))
         sizes.append(n)
         if n % 4:
             sizes.append(-n % 4)
-    return sizes, tables
+    return sizes, pieces, at
 
 
-def _new_routing(T: int, E: int, k: int, d: int | None, dev) -> Routing:
-    sizes, tables = _routing_sizes(T, E, k)
-    pieces = torch.empty(sum(sizes), dtype=torch.int32, device=dev).split_with_sizes(sizes)
-    idx, off, act, nact, chunk, nchunk, perm, inv = (pieces[i] for i in tables)
-    return Routing(topk_idx=idx.view(T, k), gates=torch.empty(T, k, dtype=torch.float32, device=dev),
-                   expert_offsets=off, active=act, num_active=nact, chunk_offsets=chunk,
-                   num_chunks=nchunk, perm_token=perm, inv_perm=inv,
-                   x_perm=None if d is None else torch.empty(T * k, d, dtype=torch.bfloat16, device=dev),
-                   E=E, k=k)
+def _split_routing(buf: torch.Tensor, x_perm: torch.Tensor | None, T: int, E: int, k: int) -> Routing:
+    sizes, pieces, _ = _routing_layout(T, E, k)
+    parts = buf.split_with_sizes(sizes)
+    gates, idx, off, act, nact, chunk, nchunk, perm, inv = [parts[i] for i in pieces]
+    return Routing(topk_idx=idx.view(T, k), gates=gates.view(torch.float32).view(T, k), expert_offsets=off,
+                   active=act, num_active=nact, chunk_offsets=chunk, num_chunks=nchunk, perm_token=perm,
+                   inv_perm=inv, x_perm=x_perm, E=E, k=k)
 
 
 def _need_routing(r: Routing, T: int, E: int, k: int, d: int | None, dev):
@@ -472,16 +471,23 @@ def moe_route_scored(logits: torch.Tensor, x: torch.Tensor | None, k: int, chunk
     with _on(dev, stream):
         need = _scored_ws_bytes(T, E, k, router, chunk_size)
         if out is None:
-            out = _new_routing(T, E, k, d, dev)
+            sizes, _, at = _routing_layout(T, E, k)
+            buf = torch.empty(sum(sizes), dtype=torch.int32, device=dev)
+            base = buf.data_ptr()
+            gates, idx, *tables = [base + o for o in at]
+            x_perm = None if d is None else torch.empty(T * k, d, dtype=torch.bfloat16, device=dev)
         else:
             _need_routing(out, T, E, k, d, dev)
+            gates, idx = _p(out.gates), _p(out.topk_idx)
+            tables = [_p(t) for t in (out.expert_offsets, out.active, out.num_active, out.chunk_offsets,
+                                      out.num_chunks, out.perm_token, out.inv_perm)]
+            x_perm = out.x_perm
         ws, wsp, wsz = _workspace(need, dev)
         _check(lib().moe_route_scored(
-            _p(logits), _p(bias), _p(x), T, E, k, d or 0, ctypes.byref(router.c()), chunk_size,
-            _p(out.topk_idx), _p(out.gates), _p(out.expert_offsets), _p(out.active), _p(out.num_active),
-            _p(out.chunk_offsets), _p(out.num_chunks), _p(out.perm_token), _p(out.inv_perm),
-            _p(out.x_perm) if x is not None else None, wsp, wsz, _here(dev)), "moe_route_scored")
-    return out
+            _p(logits), _p(bias), _p(x), T, E, k, d or 0, ctypes.byref(router.c()), chunk_size, idx, gates,
+            *tables, None if d is None else _p(x_perm), wsp, wsz, _here(dev)), "moe_route_scored")
+        # The tensors of the tables are made behind the launch (9 us of host work).
+        return _split_routing(buf, x_perm, T, E, k) if out is None else out
 
 
 def moe_route_scored_bwd(d_gates: torch.Tensor, logits: torch.Tensor, routing: Routing,
