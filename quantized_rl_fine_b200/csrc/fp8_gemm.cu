@@ -21,8 +21,8 @@
 //
 // What bounds it. Few rows: the weight stream (a block of 256 x 128 weights is
 // 32 KiB, 0.73 us at 6.56 TB/s over 148 SMs; the four MMAs take 0.3). Measured: 16
-// tokens of 8 of 48 experts, K 7168, N 4096 with SwiGLU 205 us (1.36 GB,
-// 6.6 TB/s); one token of 8 experts 43 us (5.4 TB/s: one tile a CTA, filling and
+// tokens of 8 of 48 experts, K 7168, N 4096 with SwiGLU 205 us (1.41 GB,
+// 6.9 TB/s with what L2 keeps between calls); one token of 8 experts 43 us (5.4 TB/s: one tile a CTA, filling and
 // draining its pipeline counts); 62 rows x 64 experts of 2048 x 2048 57 us (5.3 TB/s).
 // Many rows: the hand-over between tensor core and epilogue. Per 128 x 256 x 128
 // block the MMAs alone take 565 cycles, with barriers but no tensor-memory
