@@ -9,10 +9,12 @@
 // so what bounds it is latency: a warp per token, everything in registers,
 // three launches for many tokens and one for a decode batch. Measured, whole
 // call in a graph: 1 token of 384 experts in 8 groups with bias 8.7 us, 32
-// tokens 14.5, 4096 tokens of 256 experts 32.5 (about 13 of it the scan of the
+// tokens 14.5, 4096 tokens of 256 experts 21 to 25 (about 13 of it the scan of the
 // counts and the scatter), 16384 of 384 softmax without groups 39.5 (to read
 // the 25 MB of logits would take 4). FP32 keys against 64-bit keys
-// throughout: 39.5 / 88 and 32.5 / 51 us.
+// throughout: 39.5 / 88 us, and for the 4096 tokens, then in half as many
+// blocks, 32.5 / 51. A token whose keys need 64 bits takes some 5 us more, and in a
+// few thousand there are some, so the bound on the FP32 keys' error counts.
 #include <algorithm>
 
 #include "common.cuh"
@@ -153,12 +155,16 @@ __device__ __forceinline__ unsigned open_groups(const Real (&gv)[NPER], Real* wr
 //
 // Keys are compared as if in 64 bits. Without a bias the logits have the
 // keys' order and are compared themselves, exactly. With a bias the keys are
-// first formed in FP32, where each is off by less than 2^-18 (1 + |key|): expf 2
-// ulp, a sum of positive numbers at most 37 additions deep, a quotient, one
-// addition. If every two neighbours of the sorted selection, the first one
+// first formed in FP32. A sigmoid is off by less than 2^-21: with t = __expf(-l)
+// (2 + 1.173 |l| ulp), s (1 - s) (2 + 1.173 |l|) 2^-23 <= 0.63 x 2^-23, the sum 1 + t
+// 2^-24, __fdividef 2 ulp. A softmax score p is off by less than 2^-18 p, p <= 1 / z:
+// expf 2 ulp and its argument's rounding in p and in z, a sum of positive
+// numbers at most 37 additions deep, a quotient, a product. Adding the bias, or
+// two keys of a group, rounds by 2^-24 of the sum, less than the 2^-22 allowed
+// for it (top: the largest key). If every two neighbours of the sorted selection, the first one
 // left out, and the groups around the cut lie further apart than twice that,
 // the selection is the one in 64 bits. Where only neighbours are too close
-// (about one token in 100 for normal logits), the experts that may belong to
+// (one token in some hundreds for normal logits), the experts that may belong to
 // the selection, at most 32, are ordered by their keys in 64 bits, one a lane;
 // otherwise (groups too close, more than 32 equal keys, masked experts
 // reached) the whole token is done again in 64 bits.
@@ -223,7 +229,8 @@ __device__ __forceinline__ void select_token(const float* __restrict__ row, cons
     if (scores) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(full, top, o));
-      err = 3.814697265625e-6f * (1.0f + top);   // 2^-18
+      // 2^-18 / z or 2^-21, and 2^-22 top
+      err = (softmax ? 3.814697265625e-6f * zinv : 4.76837158203125e-7f) + 2.384185791015625e-7f * top;
     }
     if (grouped) {
       float gap;
@@ -415,11 +422,12 @@ __device__ __forceinline__ float gate_of(const float* __restrict__ row, int idx,
   return static_cast<float>(rt.scale * (sum64 > 0.0 ? s64 / sum64 : 0.0));
 }
 
-// tpb tokens per block; block_counts == nullptr skips the per-block histogram.
+// tpb tokens per block, or per cluster of two blocks (parts = 2), which add
+// their histograms; block_counts == nullptr skips the histogram.
 template <int NPER>
 __global__ void __launch_bounds__(kScoredThreads, 1)
 route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ bias, int T, int E, int k, int tpb,
-                    int row_el, moe_router rt, int32_t* __restrict__ topk_idx, float* __restrict__ gates,
+                    int parts, int row_el, moe_router rt, int32_t* __restrict__ topk_idx, float* __restrict__ gates,
                     int32_t* __restrict__ block_counts) {
   extern __shared__ double scored_sm[];   // [warps][row_el] group scratch; then [E] histogram
   grid_dependency_wait();
@@ -431,8 +439,10 @@ route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ 
     for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int u = warp; u < tpb; u += warps) {
-    const int t = blockIdx.x * tpb + u;
+  const int rank = parts == 2 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int group = static_cast<int>(blockIdx.x) / parts, mine = tpb / parts;
+  for (int u = warp; u < mine; u += warps) {
+    const int t = group * tpb + rank * mine + u;
     if (t >= T) break;
     const float* row = logits + static_cast<int64_t>(t) * E;
     float mx;
@@ -449,9 +459,18 @@ route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ 
     }
   }
   if (!with_hist) return;
-  __syncthreads();
-  for (int e = threadIdx.x; e < E; e += blockDim.x)
-    block_counts[static_cast<int64_t>(blockIdx.x) * E + e] = hist[e];
+  if (parts == 2) cluster_sync_all(); else __syncthreads();
+  if (rank == 0)
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+      int32_t n = hist[e];
+      if (parts == 2) {
+        int32_t other;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(other) : "r"(cluster_addr(smem_u32(&hist[e]), 1)) : "memory");
+        n += other;
+      }
+      block_counts[static_cast<int64_t>(group) * E + e] = n;
+    }
+  if (parts == 2) cluster_sync_all();     // (the other block's counts have been read)
 }
 
 // Up to 32 tokens (a decode batch) in one block and one launch: a warp per
@@ -604,13 +623,28 @@ cudaError_t launch_route_scored(const float* logits, const float* bias, const vo
    : nper <= 12 ? CALL_(12)             \
    : nper <= 16 ? CALL_(16) : CALL_(32))
   // (always to the same value, so that calls from several host threads agree)
-  auto go = [&](auto kern, int blocks, int threads, size_t sm, auto... args) {
+  auto go = [&](auto kern, int blocks, int threads, int parts, size_t sm, auto... args) {
     if (sm > 32 * 1024) {
       const cudaError_t e =
           cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoredMaxSmem);
       if (e != cudaSuccess) return e;
     }
-    return launch_pdl(kern, dim3(blocks), dim3(threads), sm, s, args...);
+    if (parts == 1) return launch_pdl(kern, dim3(blocks), dim3(threads), sm, s, args...);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = parts;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = sm;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
   };
   // one warp's group scratch, in doubles
   const int row_el = rt.groups > 1 ? group_pitch(E, rt.groups) * rt.groups : 0;
@@ -620,7 +654,7 @@ cudaError_t launch_route_scored(const float* logits, const float* bias, const vo
                               : static_cast<int>(std::min<size_t>(kScoredWarps, (kScoredMaxSmem - 4096) / row_sm));
   if (T <= std::min(kSmallTokens, fit) && x == nullptr) {
 #define MOEQ_SMALL(N_)                                                                                             \
-  go(route_scored_small_kernel<N_>, 1, kScoredThreads, row_sm* T, logits, bias, T, E, k, row_el, rt, chunk_size, topk_idx, gates, \
+  go(route_scored_small_kernel<N_>, 1, kScoredThreads, 1, row_sm* T, logits, bias, T, E, k, row_el, rt, chunk_size, topk_idx, gates, \
      offsets, active, num_active, chunk_offsets, num_chunks, perm_token, inv_perm)
     return MOEQ_BY_NPER(MOEQ_SMALL);
 #undef MOEQ_SMALL
@@ -630,10 +664,19 @@ cudaError_t launch_route_scored(const float* logits, const float* bias, const vo
   const int tpb = small ? fit : route_tokens_per_block();
   const int nblk = (T + tpb - 1) / tpb;
   int32_t* hist_out = small ? nullptr : block_counts;
+  // Two blocks (a cluster, one token a warp instead of two) per histogram while
+  // all of them can run at once, which halves the selection's share; above
+  // that the cluster only costs. Measured (one / two blocks, us): 2048 tokens of
+  // 256 experts in groups 33.2 / 24.7, 4096 33.5 / 26.0, 8192 35.0 / 37.2; 6000 of
+  // 384 without groups 25.1 / 28.4, 16384 41.9 / 50.0.
+  int sms = 0;
+  cudaError_t err = route_prepare_device(&sms);
+  if (err != cudaSuccess) return err;
+  const int parts = !small && 2 * nblk <= sms ? 2 : 1;
   const size_t sm = row_sm * fit + (small ? 0 : sizeof(int32_t) * E);
 #define MOEQ_LARGE(N_) \
-  go(route_scored_kernel<N_>, nblk, 32 * fit, sm, logits, bias, T, E, k, tpb, row_el, rt, topk_idx, gates, hist_out)
-  const cudaError_t err = MOEQ_BY_NPER(MOEQ_LARGE);
+  go(route_scored_kernel<N_>, nblk * parts, 32 * fit, parts, sm, logits, bias, T, E, k, tpb, parts, row_el, rt, topk_idx, gates, hist_out)
+  err = MOEQ_BY_NPER(MOEQ_LARGE);
 #undef MOEQ_LARGE
 #undef MOEQ_BY_NPER
   if (err != cudaSuccess) return err;
