@@ -30,8 +30,8 @@
 // tensor-memory loads and the release follow one another, and only two buffers
 // of 256 columns fit. 768 rows x 48 experts, K 7168, N 4096: 1037 us at full
 // clocks (2.09 PFLOP/s), 1190 under the power cap; backward 1074 / 1248; SwiGLU
-// 1060 / 1219, with checkpoint 1132 / 1312 (its epilogue, about 5 us a tile, is
-// not overlapped: the accumulators are in registers). SwiGLU backward 620 us for
+// 1040 / 1225, with checkpoint 1078 / 1275 (its epilogue, about 2 us a tile, is
+// not overlapped: the accumulators are in registers). SwiGLU backward 607 us for
 // half the work.
 // Tried, without gain: 128-column tiles or a column split with their own barriers
 // (the time per hand-over stays), two MMA issuers, spinning waits, tensor-memory
@@ -305,14 +305,6 @@ __device__ __forceinline__ uint32_t quantize_bf16x4(uint32_t p0, uint32_t p1, fl
                     __uint_as_float(p1 << 16) * inv, __uint_as_float(p1 & 0xffff0000u) * inv);
 }
 
-// Copies `bytes` (a multiple of 16) of this thread's staging slot to global
-// memory; the thread wrote them itself, so only its own writes need ordering
-// before the copy (fence_proxy_async_smem).
-__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src),
-               "r"(bytes)
-               : "memory");
-}
 // `bytes` (a multiple of 16) from global to shared memory, counted on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile(
@@ -320,12 +312,27 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       "l"(src), "r"(bytes), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// This thread's copies have read shared memory / have finished.
-__device__ __forceinline__ void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+
+// Stores BYTES of each of the warp's 32 staging slots, rows [0, valid), to rows
+// of ld bytes at dst: BYTES / 16 neighbouring lanes a row, so that a store
+// instruction writes whole sectors of several rows. (Bulk copies of a row's 64
+// bytes, one a lane, took 2 us a tile more: 1536 rows x 48 experts, K 2048, N 7168,
+// SwiGLU with checkpoint 1485 us instead of 1280.)
+template <int BYTES>
+__device__ __forceinline__ void store_rows(uint8_t* dst, int64_t ld, uint32_t slot0, int valid, int lane,
+                                           uint32_t bytes = BYTES) {
+  constexpr int L = BYTES / 16, kRowsAtOnce = 32 / L;
+  const int r0 = lane / L;
+  const uint32_t c = 16u * (lane % L);
+  uint32_t src = slot0 + static_cast<uint32_t>(r0) * kSlot8 + c;
+  uint8_t* d = dst + r0 * ld + c;
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    if (r0 + i * kRowsAtOnce < valid && c < bytes) *reinterpret_cast<uint4*>(d) = lds128(src);
+    src += kRowsAtOnce * kSlot8;
+    d += kRowsAtOnce * ld;
+  }
 }
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // a += s * v on two FP32 values at once (each rounded as one fused multiply-add).
 __device__ __forceinline__ void fma2(uint64_t& a, uint64_t s, uint32_t v0, uint32_t v1) {
@@ -682,11 +689,7 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
         if constexpr (kGluBwd) {
           // Once the previous tile's output has left the staging slots, warp 3
           // brings this tile's g and u there while the product runs.
-          if (kb == min(2, p.nkb - 1)) {
-            bulk_wait_read();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(slot_free);
-          }
+          if (kb == min(2, p.nkb - 1) && lane == 0) mbar_arrive(slot_free);
         }
         const int b = static_cast<int>(it & 1);
         const bool r = mbar_wait8(acc_full(b), static_cast<uint32_t>((it >> 1) & 1), abort_at);
@@ -739,7 +742,16 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
 #pragma unroll
         for (int j = 0; j < 64; ++j) unpair2(acc2[j], acc[2 * j], acc[2 * j + 1]);
       }
-      if constexpr (!kGluBwd) bulk_wait_read();  // the previous tile's output has left the slot
+      // The warp's rows are the first `valid` lanes, from row `first`. (Asked for
+      // behind the arithmetic, which needs the registers.)
+      const uint32_t slot0 = slot - static_cast<uint32_t>(lane) * kSlot8;
+      int valid = 0;
+      int64_t first = 0;
+      auto warp_rows = [&] {
+        __syncwarp();                        // the slots have been written
+        valid = __popc(__ballot_sync(0xffffffffu, cur_row >= 0));
+        first = __shfl_sync(0xffffffffu, cur_row, 0);
+      };
 
       if constexpr (kGlu) {
         // acc[0..63] gate, acc[64..127] up of features f0 ..; the slot holds
@@ -770,16 +782,14 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
         const int e = fp8_block_exp(m);
         quantize32(acc, exp2_int(-e), slot);
         quantize32(acc + 32, exp2_int(-e), slot + 32u);
-        fence_proxy_async_smem();
-        if (cur_row >= 0) {
-          bulk_store(p.out + static_cast<int64_t>(cur_row) * f_half + f0, slot, 64);
-          if (p.saved != nullptr) {
-            uint8_t* sv = p.saved + static_cast<int64_t>(cur_row) * p.N + f0;
-            bulk_store(sv, slot + 64u, 64);
-            bulk_store(sv + f_half, slot + 128u, 64);
-          }
-          if (wg == 0) p.out_scales[static_cast<int64_t>(cur_ft) * p.M + cur_row] = exp2_int(e);
+        warp_rows();
+        store_rows<64>(p.out + first * f_half + f0, f_half, slot0, valid, lane);
+        if (p.saved != nullptr) {
+          uint8_t* sv = p.saved + first * p.N + f0;
+          store_rows<64>(sv, p.N, slot0 + 64u, valid, lane);
+          store_rows<64>(sv + f_half, p.N, slot0 + 128u, valid, lane);
         }
+        if (wg == 0 && cur_row >= 0) p.out_scales[static_cast<int64_t>(cur_ft) * p.M + cur_row] = exp2_int(e);
       } else if constexpr (kGluBwd) {
         // dh of features f0 .. f0 + 127; the slot holds [128 B g][128 B u][4 + 4
         // scales] and then [128 B dg][128 B du].
@@ -852,11 +862,13 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
             sts128(slot + 16u * c, og[0], og[1], og[2], og[3]);
             sts128(slot + 128u + 16u * c, ou[0], ou[1], ou[2], ou[3]);
           }
-          fence_proxy_async_smem();
+          warp_rows();
+          if (f0 < K) {
+            uint8_t* dst = p.out + first * (2 * K) + f0;
+            store_rows<128>(dst, 2 * K, slot0, valid, lane);
+            store_rows<128>(dst + K, 2 * K, slot0 + 128u, valid, lane);
+          }
           if (cur_row >= 0 && f0 < K) {
-            uint8_t* dst = p.out + static_cast<int64_t>(cur_row) * (2 * K) + f0;
-            bulk_store(dst, slot, 128);
-            bulk_store(dst + K, slot + 128u, 128);
             const int64_t blk = f0 / 128;
             p.out_scales[blk * p.M + cur_row] = exp2_int(eg);
             p.out_scales[(blk + K / 128) * p.M + cur_row] = exp2_int(eu);
@@ -870,14 +882,15 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
           sts128(slot + 16u * c, pack_bf16x2(acc[8 * c], acc[8 * c + 1]),
                  pack_bf16x2(acc[8 * c + 2], acc[8 * c + 3]), pack_bf16x2(acc[8 * c + 4], acc[8 * c + 5]),
                  pack_bf16x2(acc[8 * c + 6], acc[8 * c + 7]));
-        fence_proxy_async_smem();
-        if (cur_row >= 0 && f0 < F)          // F % 16 == 0: whole 32-byte pieces
-          bulk_store(p.out + 2 * (static_cast<int64_t>(cur_row) * F + f0), slot,
-                     2u * static_cast<uint32_t>(min(128, F - f0)));
+        warp_rows();
+        if (f0 < F)                          // F % 16 == 0: whole 32-byte pieces
+          store_rows<256>(p.out + 2 * (first * F + f0), 2 * static_cast<int64_t>(F), slot0, valid, lane,
+                          2u * static_cast<uint32_t>(min(128, F - f0)));
       }
-      bulk_commit();
+      __syncwarp();                          // the slots have been read
+      // (SwiGLU backward: the next rows come there by bulk copy)
+      if constexpr (kGluBwd) fence_proxy_async_smem();
     }
-    bulk_wait_all();
   }
 
   tc_fence_before();
