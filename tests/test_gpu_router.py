@@ -276,6 +276,27 @@ def test_many_groups(E, groups, T):
         _check(logits, 4, _spec(score="sigmoid", groups=groups, topk_groups=5, group_top=gt), b)
 
 
+@pytest.mark.parametrize("T", [1025, 1056, 1057, 1089, 4736, 4737, 9001])
+@pytest.mark.parametrize("E,groups", [(64, 1), (384, 8)])
+def test_many_tokens(T, E, groups):
+    """One and two blocks per histogram of 64 tokens, blocks without tokens among them."""
+    g = torch.Generator().manual_seed(E + T)
+    logits = torch.randn((T, E), generator=g)
+    _check(logits, 6, _spec(score="sigmoid", groups=groups, topk_groups=max(1, groups // 2)), 0.1 * torch.randn(E, generator=g))
+
+
+@pytest.mark.parametrize("score,spread", [("sigmoid", 2e-5), ("sigmoid", 2e-6), ("softmax", 2e-4), ("softmax", 2e-5)])
+@pytest.mark.parametrize("groups,group_top", [(1, 1), (8, 1), (8, 2)])
+def test_keys_within_the_errors_of_single_precision(score, spread, groups, group_top):
+    """Keys so close that single precision settles some selections, a few need 64 bits for their candidates and others for all."""
+    T, E = 1500, 256
+    g = torch.Generator().manual_seed(int(spread * 1e7) + groups + group_top)
+    logits = 0.5 + spread * torch.randn((T, E), generator=g)
+    bias = (0.25 if score == "sigmoid" else 1 / 256) * spread * torch.randn(E, generator=g)
+    bias[::2] *= 40.0                                   # and gaps between some of them
+    _check(logits, 8, _spec(score=score, groups=groups, topk_groups=max(1, groups // 2), group_top=group_top), bias)
+
+
 def test_infinite_and_huge_biases():
     T, E, k = 40, 48, 5
     g = torch.Generator().manual_seed(12)
