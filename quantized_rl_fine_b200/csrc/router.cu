@@ -166,7 +166,7 @@ __device__ __forceinline__ unsigned open_groups(const Real (&gv)[NPER], Real* wr
 // the selection is the one in 64 bits. Where only neighbours are too close
 // (one token in some hundreds for normal logits), the experts that may belong to
 // the selection, at most 32, are ordered by their keys in 64 bits, one a lane;
-// otherwise (groups too close, more than 32 equal keys, masked experts
+// otherwise (groups too close, more than 32 candidates, masked experts
 // reached) the whole token is done again in 64 bits.
 template <int NPER>
 __device__ __forceinline__ void select_token(const float* __restrict__ row, const float* __restrict__ bias, int E,
@@ -245,7 +245,8 @@ __device__ __forceinline__ void select_token(const float* __restrict__ row, cons
     }
     // k rounds; with inexact keys more, while a key may still belong to the
     // selection (it is within reach of the k-th), and one for the first that
-    // cannot. Lane j holds the j-th candidate.
+    // cannot. Lane j holds the j-th candidate; a 33rd, which no lane holds, is
+    // still looked at: with one within reach, close keys need the whole token in 64 bits.
     // Each lane keeps its three best keys in order; a lane that has given all
     // three (rare: four of the selected experts in one lane) looks through its
     // keys again for those behind the last one it gave.
@@ -270,7 +271,7 @@ __device__ __forceinline__ void select_token(const float* __restrict__ row, cons
     };
     refill(0xffffffffu, 0x7fffffff);
     int given = 0;
-    const int rounds = bias ? min(32, E) : k;
+    const int rounds = bias ? min(33, E) : k;
     float last = 0.0f, reach = 0.0f;
     int count = 0;
     bool close = false, odd = false;      // neighbours too close; only 64 bits will do
@@ -308,7 +309,7 @@ __device__ __forceinline__ void select_token(const float* __restrict__ row, cons
       }
     }
     if (bias && (close || odd)) {
-      if (odd || count == 32 || !(err < INFINITY)) {
+      if (odd || count > 32 || !(err < INFINITY)) {
         sure = false;
       } else if (sure) {
         // Order the candidates by their keys in 64 bits.

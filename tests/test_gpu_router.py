@@ -396,3 +396,38 @@ def test_refusals_of_wrong_tensors():
         moeq.moe_combine_bwd(rows[:4], rows, r, out=rows)              # in place
     with pytest.raises(ValueError):
         moeq.moe_combine_bwd(rows[:3], rows, r)
+
+
+# ----------------------------------------------------------------------------- k = 32 with a bias
+
+def test_the_first_expert_left_out_of_32_is_compared_too():
+    """31 experts far ahead by their bias; the 32nd place lies between logits 12 and the next float, whose
+    sigmoids are equal in single precision and differ by 7e-12 in 64 bits: the larger one, of the higher id, wins."""
+    E, k = 40, 32
+    logits = torch.linspace(-3, 3, E).repeat(5, 1)
+    logits[:, 31] = 12.0
+    logits[:, 32] = torch.nextafter(torch.tensor(12.0), torch.tensor(13.0))
+    bias = torch.full((E,), -1.0)
+    bias[:31], bias[31:33] = 2.0, 0.0
+    r, topk = _check(logits, k, _spec(score="sigmoid"), bias)
+    assert np.all(topk[:, 31] == 32)
+
+
+@pytest.mark.parametrize("E,groups", [(33, 1), (40, 1), (64, 1), (65, 1), (384, 1), (384, 8), (1024, 4)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("k", [31, 32])
+def test_near_ties_around_the_last_of_32_places(E, groups, score, k):
+    """Some experts ahead by a clear margin (none to 31), all others within a few floats of one another: the
+    last places are decided in 64 bits, with the candidates filling the warp's 32 lanes or more."""
+    T = 64
+    g = torch.Generator().manual_seed(E + k + groups)
+    step = 2.0 ** -23 if score == "softmax" else 2.0 ** -20
+    base = 1.0 if score == "softmax" else 12.0
+    logits = base + step * torch.stack([torch.randperm(E, generator=g) for _ in range(T)]).float()
+    bias = torch.zeros(E)
+    for i, e in enumerate(torch.randperm(E, generator=g)[:31].tolist()):
+        bias[e] = 2.0 + 0.01 * i
+    spec = _spec(score=score, groups=groups, topk_groups=groups)
+    _check(logits, k, spec, bias)
+    bias[bias > 2.2] = 0.0                             # 20 ahead
+    _check(logits, k, spec, bias)
