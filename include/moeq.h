@@ -493,6 +493,7 @@ int32_t moe_nvtx_enabled(void);
  * moe_test_set_wait_budget: sets the cycle budget of every pipeline wait
  * (default about one second); a tiny budget makes the waits of the next
  * GEMM run out so that the error path can be tested. 0 restores the default.
+ * The FP8 products count in steps of 1024 cycles and wait 2^41 cycles at most.
  */
 moe_status moe_test_dequant(const void* packed, const void* scales, int64_t R, int32_t K,
                             int32_t fmt, void* out, void* stream);

@@ -48,6 +48,7 @@
 
 #include "fp8.cuh"
 #include "fp8_gemm.cuh"
+#include "fp8_wait.cuh"
 
 namespace moeq {
 
@@ -135,16 +136,16 @@ __device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
-// mbar_wait with few registers held: 32-bit clock, the abort flag by its
-// shared-memory address, the budget (2^32 - 1 cycles at most) read when asked.
+// mbar_wait with few registers held: time in 32 bits, the abort flag by its
+// shared-memory address, the budget (2^41 cycles at most) read when asked.
 __device__ __forceinline__ bool mbar_wait8(uint32_t bar, uint32_t parity, uint32_t abort_flag) {
   if (mbar_try_wait_sleep(bar, parity, kWaitSleepNs)) return true;
-  const uint32_t t0 = static_cast<uint32_t>(clock());
+  const uint32_t t0 = wait_units(clock64());
   while (!mbar_try_wait_sleep(bar, parity, kWaitSleepNs)) {
     uint32_t gone;
     asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(gone) : "r"(abort_flag));
     if (gone) return false;
-    if (static_cast<uint32_t>(clock()) - t0 > *reinterpret_cast<volatile long long*>(&g_wait_budget)) {
+    if (wait_spent(t0, wait_units(clock64()), *reinterpret_cast<volatile long long*>(&g_wait_budget))) {
       raise_device_error(MOE_DEVERR_WAIT_TIMEOUT);
       asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort_flag), "r"(1u));
       return false;
