@@ -40,9 +40,9 @@
 // The backward reads the same weights in place, as the MN-major B operand:
 // features contiguous, 128-byte swizzled blocks of 128 features.
 //
-// Every wait is bounded; on a timeout the kernel records a device error, lets
-// its copies and MMAs in flight finish (again bounded), frees tensor memory
-// and returns.
+// Every wait is bounded; on a timeout the kernel records a device error, all
+// roles stop (in a pair, both CTAs'), the copies and MMAs in flight finish (again
+// bounded), tensor memory is freed and the kernel returns.
 #include <algorithm>
 #include <atomic>
 
@@ -137,7 +137,9 @@ __device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
 }
 
 // mbar_wait with few registers held: time in 32 bits, the abort flag by its
-// shared-memory address, the budget (2^41 cycles at most) read when asked.
+// shared-memory address, the budget (2^41 cycles at most) read when asked. In
+// a pair both CTAs' flags are set, so that the other one soon stops too.
+template <int PAIR>
 __device__ __forceinline__ bool mbar_wait8(uint32_t bar, uint32_t parity, uint32_t abort_flag) {
   if (mbar_try_wait_sleep(bar, parity, kWaitSleepNs)) return true;
   const uint32_t t0 = wait_units(clock64());
@@ -147,12 +149,29 @@ __device__ __forceinline__ bool mbar_wait8(uint32_t bar, uint32_t parity, uint32
     if (gone) return false;
     if (wait_spent(t0, wait_units(clock64()), *reinterpret_cast<volatile long long*>(&g_wait_budget))) {
       raise_device_error(MOE_DEVERR_WAIT_TIMEOUT);
-      asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort_flag), "r"(1u));
+      if constexpr (PAIR) {
+        for (uint32_t r = 0; r < 2; ++r)
+          asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(abort_flag, r)), "r"(1u)
+                       : "memory");
+      } else {
+        asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort_flag), "r"(1u));
+      }
       return false;
     }
   }
   return true;
 }
+
+// The full barriers of a CTA's stages, for close_fills.
+struct FullBars8 {
+  uint32_t first, stage_bytes;
+  __device__ __forceinline__ void add_bytes(uint32_t s) const {
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(first + 8u * s), "r"(stage_bytes)
+                 : "memory");
+  }
+  __device__ __forceinline__ void arrive(uint32_t s) const { mbar_arrive_expect_tx(first + 8u * s, stage_bytes); }
+  __device__ __forceinline__ void wait(uint32_t s, uint32_t parity) const { mbar_drain(first + 8u * s, parity); }
+};
 
 // Instruction descriptor, kind::f8f6f4: FP32 D, e4m3 A and B (format 0).
 __host__ __device__ constexpr uint32_t idesc_f8(uint32_t M, uint32_t N, uint32_t b_mn) {
@@ -407,6 +426,8 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (bars - base) + 8u * (2 * S + 10));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const uint32_t abort_at = bars + 8u * (2 * S + 10) + 4u;
+  // What the copying warps have begun: stage fills, and tiles' checkpoint rows.
+  const uint32_t fills_at = abort_at + 4u, ck_tiles_at = abort_at + 8u;
   float* row_amax = reinterpret_cast<float*>(tmem_slot + 4);                 // [2 tiles][2][128]
   int32_t* warp_tot = reinterpret_cast<int32_t*>(row_amax + 4 * kRows8);     // [32]
   TileList8 list;
@@ -462,8 +483,7 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
       const uint64_t pol_a = l2_policy_evict_last();
       const uint64_t pol_w = p.w_once ? l2_policy_evict_first() : l2_policy_evict_last();
       int st = 0;
-      uint32_t ph = 0;
-      long long issued = 0;
+      uint32_t ph = 0, fills = 0;
       bool ok = true;
       Tile8 tl;
       tl.a = 0;
@@ -472,7 +492,7 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
         const int c0 = kGlu ? tl.ft * 128 : tl.ft * 256;       // features of the two boxes
         const int c1 = kGlu ? f_half + tl.ft * 128 : c0 + 128;
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait8(empty(st), ph ^ 1u, abort_at)) { ok = false; break; }
+          if (!mbar_wait8<PAIR>(empty(st), ph ^ 1u, abort_at)) { ok = false; break; }
           // A pair's stages are one: both CTAs' copies count on the even CTA's
           // barrier, which is where the MMAs are issued.
           uint32_t bar = full(st);
@@ -488,15 +508,11 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
             tma_load8<PAIR>(B_at(st), &tm_w, bar, kb * 128, cf, tl.e, pol_w);
             if constexpr (!PAIR) tma_load8<PAIR>(B_at(st) + kBoxBytes, &tm_w, bar, kb * 128, c1, tl.e, pol_w);
           }
-          ++issued;
+          ++fills;
           if (++st == S) { st = 0; ph ^= 1u; }
         }
       }
-      if (!ok && rank == 0) {
-        // Copies in flight (a pair's odd CTA's too) land before the CTAs can exit.
-        for (long long g = issued > S ? issued - S : 0; g < issued; ++g)
-          mbar_drain(full(static_cast<int>(g % S)), static_cast<uint32_t>((g / S) & 1));
-      }
+      sts32(fills_at, fills);
     }
     __syncwarp();
   } else if (warp == 1 && rank == 0) {
@@ -507,7 +523,7 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
     uint32_t it = 0;                      // reduction blocks handed over (buffer it % 2)
     bool ok = true;
     auto wait_w = [&](uint32_t bar, uint32_t parity) {
-      const bool r = mbar_wait8(bar, parity, abort_at);
+      const bool r = mbar_wait8<PAIR>(bar, parity, abort_at);
       return __shfl_sync(0xffffffffu, r ? 1 : 0, 0) != 0;
     };
     auto commit = [](uint32_t bar) {
@@ -585,7 +601,7 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
       };
       auto step = [&](Set& x, int kb) {
         const int b = static_cast<int>(it & 1);
-        ok = mbar_wait8(sc_free(b), ((it >> 1) & 1) ^ 1u, abort_at);
+        ok = mbar_wait8<PAIR>(sc_free(b), ((it >> 1) & 1) ^ 1u, abort_at);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
 #pragma unroll
@@ -613,15 +629,13 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
     // ------------------------------------------------------------ checkpoint rows
     // For the staging slots (half, row) of each tile: the row's 128 bytes
     // of g and of u by bulk copy, and its four plus four E8M0 scales.
-    bool ok = true, any = false;
-    int li = 0;
+    uint32_t li = 0;
     Tile8 tl;
     tl.a = 0;
     for (int t = t_first; t < total; t += t_step, ++li) {
       tl = tile8_at<FORM>(list, t, tl.a, rank);
-      ok = mbar_wait8(slot_free, static_cast<uint32_t>(li & 1), abort_at);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
+      const bool ok = mbar_wait8<PAIR>(slot_free, li & 1u, abort_at);
+      if (!__all_sync(0xffffffffu, ok)) break;
       uint32_t valid = 0;
 #pragma unroll 1
       for (int i = 0; i < kActive; ++i) {
@@ -638,7 +652,6 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
         sts64(stg_base + static_cast<uint32_t>(i * 32 + lane) * kSlot8 + 256u, g, u);
       }
       mbar_arrive_expect_tx(gu_bar, 256 * valid);
-      any = true;
 #pragma unroll 1
       for (int i = 0; i < kActive; ++i) {
         const int row = tl.row0 + (i % kQuarters) * 32 + lane, f0 = tl.ft * 256 + (i / kQuarters) * 128;
@@ -649,8 +662,7 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
         bulk_load(dst + 128u, src + p.K, 128, gu_bar);
       }
     }
-    // an abort after some copies: they land before the CTA can exit
-    if (!ok && any) mbar_drain(gu_bar, static_cast<uint32_t>((li - 1) & 1));
+    if (lane == 0) sts32(ck_tiles_at, li);
     __syncwarp();
   } else if (warp >= kEpiWarp8) {
     // ------------------------------------------------------------ scaled sum and epilogue
@@ -693,7 +705,7 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
           if (kb == min(2, p.nkb - 1) && lane == 0) mbar_arrive(slot_free);
         }
         const int b = static_cast<int>(it & 1);
-        const bool r = mbar_wait8(acc_full(b), static_cast<uint32_t>((it >> 1) & 1), abort_at);
+        const bool r = mbar_wait8<PAIR>(acc_full(b), static_cast<uint32_t>((it >> 1) & 1), abort_at);
         if (!__shfl_sync(0xffffffffu, r ? 1 : 0, 0)) { ok = false; break; }
         tc_fence_after();
         const uint32_t tb = tq + static_cast<uint32_t>(b) * 256u;
@@ -733,7 +745,7 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
         }
       }
       if constexpr (kGluBwd) {
-        if (ok) ok = mbar_wait8(gu_bar, li, abort_at);
+        if (ok) ok = mbar_wait8<PAIR>(gu_bar, li, abort_at);
         ok = __all_sync(0xffffffffu, ok);
       }
       if (!ok) break;
@@ -777,7 +789,7 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
         xch[wg * kRows8 + r_in] = m;
         __syncwarp();
         if (lane == 0) mbar_arrive(amax_bar);
-        const bool met = mbar_wait8(amax_bar, li, abort_at);
+        const bool met = mbar_wait8<PAIR>(amax_bar, li, abort_at);
         if (!__shfl_sync(0xffffffffu, met ? 1 : 0, 0)) break;
         m = fmaxf(m, xch[(wg ^ 1) * kRows8 + r_in]);
         const int e = fp8_block_exp(m);
@@ -900,6 +912,25 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
   // and write both CTAs, have drained and both epilogues are done.
   if constexpr (PAIR) cluster_sync_all(); else __syncthreads();
   tc_fence_after();
+  if (*abort_flag) {
+    // A wait has run out, in this CTA or in the pair's other one, and every role
+    // has stopped, each where it was: copies may be in flight for which nobody
+    // has waited. They land before a CTA can exit.
+    if (threadIdx.x == 0 && rank == 0) {
+      const uint32_t mine = lds32(fills_at);
+      uint32_t other = mine;
+      if constexpr (PAIR)
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(other) : "r"(cluster_addr(fills_at, 1)) : "memory");
+      FullBars8 b = {full(0), kStage8};
+      close_fills(mine, other, S, b);
+    }
+    if (kGluBwd && threadIdx.x == 96) {
+      const uint32_t n = lds32(ck_tiles_at);
+      if (n > 0) mbar_drain(gu_bar, (n - 1) & 1u);
+    }
+    __syncwarp();
+    if constexpr (PAIR) cluster_sync_all(); else __syncthreads();
+  }
   if (warp == 1) {
     if constexpr (PAIR) tmem_dealloc_pair(tmem_base, 512); else tmem_dealloc(tmem_base, 512);
   }

@@ -45,3 +45,69 @@ int main() {
 def test_every_budget_ends_a_wait_and_none_too_early(tmp_path):
     """Budgets past 32 bits among them: the longest a wait can take is 2^41 cycles, whatever was set."""
     run_on_host(tmp_path, BUDGET)
+
+
+CLOSE = r"""
+// Barriers as the hardware counts them: a phase completes when its arrivals and its bytes are all there.
+struct Barrier {
+  int pending = 1, phase = 0;
+  long long tx = 0;
+  void settle() { if (pending == 0 && tx == 0) { pending = 1; ++phase; } }
+  void arrive(long long bytes) { tx += bytes; --pending; settle(); }
+  void bytes(long long n) { tx -= n; settle(); }
+};
+constexpr int kBytes = 32768;
+static int bad = 0;
+struct Model {
+  uint32_t S;
+  Barrier bar[8];
+  int in_flight[8] = {0};          // copies that have not landed, by stage
+  void land(uint32_t s) { if (in_flight[s] > 0) { --in_flight[s]; bar[s].bytes(kBytes); } }
+  void add_bytes(uint32_t s) { bar[s].bytes(kBytes); }
+  void arrive(uint32_t s) { bar[s].arrive(kBytes); }
+  bool done(uint32_t s, uint32_t parity) const { return (bar[s].phase & 1) != (int)parity; }
+  void wait(uint32_t s, uint32_t parity) {
+    while (in_flight[s] > 0) {
+      if (done(s, parity)) { std::printf("over before the copies\n"); bad = 1; return; }
+      land(s);
+    }
+    if (!done(s, parity)) { std::printf("never over\n"); bad = 1; }
+  }
+};
+// A pair (or a CTA alone) stopped at a random point: `used` fills were consumed, the even CTA has begun n0 and the
+// odd one n1 of them, and some of the copies that are not consumed have landed.
+static void stopped(uint32_t S, uint32_t used, uint32_t n0, uint32_t n1, bool pair) {
+  Model m;
+  m.S = S;
+  const uint32_t end = n0 > n1 ? n0 : n1;
+  for (uint32_t g = 0; g < end; ++g) {
+    Barrier& b = m.bar[g % S];
+    const int even = g < n0, odd = pair && g < n1;
+    const bool odd_first = std::rand() & 1;
+    if (odd && odd_first) { if (g < used || (std::rand() & 1)) b.bytes(kBytes); else ++m.in_flight[g % S]; }
+    if (even) {
+      b.arrive(pair ? 2 * kBytes : kBytes);
+      if (g < used || (std::rand() & 1)) b.bytes(kBytes); else ++m.in_flight[g % S];
+    }
+    if (odd && !odd_first) { if (g < used || (std::rand() & 1)) b.bytes(kBytes); else ++m.in_flight[g % S]; }
+  }
+  close_fills(n0, pair ? n1 : n0, S, m);
+  for (uint32_t s = 0; s < S; ++s)
+    if (m.in_flight[s]) { std::printf("copies left: S %u used %u begun %u %u\n", S, used, n0, n1); bad = 1; }
+}
+int main() {
+  for (uint32_t S = 3; S <= 5; ++S)
+    for (uint32_t used = 0; used < 14; ++used)
+      for (uint32_t a = 0; a <= S; ++a)
+        for (uint32_t b = 0; b <= S; ++b)
+          for (int pair = 0; pair < 2; ++pair)
+            for (int i = 0; i < 20; ++i) stopped(S, used, used + a, pair ? used + b : used + a, pair);
+  return bad;
+}
+"""
+
+
+def test_a_stopped_product_waits_for_every_copy_that_was_begun(tmp_path):
+    """Wherever the copying warps of a CTA or of a pair's two stopped, against barriers counted in a model: no wait
+    is over before the stage's copies have landed, and none lasts for ever."""
+    run_on_host(tmp_path, CLOSE)

@@ -507,3 +507,48 @@ def test_refusals_of_wrong_rows_and_weights():
         moeq.moe_quantize_fp8_rows(torch.zeros((4, 24), dtype=torch.bfloat16, device=DEV))
     with pytest.raises(ValueError):
         moeq.moe_quantize_fp8_rows(torch.zeros((5, 32), dtype=torch.bfloat16, device=DEV), r)
+
+
+@pytest.mark.parametrize("epi", ["none", "glu", "bwd", "glu_bwd"])
+@pytest.mark.parametrize("form", ["0", "1", "2", "3"])
+def test_products_stopped_anywhere_leave_the_next_call_clean(form, epi, monkeypatch):
+    """Budgets from about a microsecond up, so that different roles give up at different points (in a pair, in either
+    CTA): a product that reports no timeout has all its bits, and the next one with the default budget has them too."""
+    monkeypatch.setenv("MOEQ_F8FORM", form)
+    g = torch.Generator(device=DEV).manual_seed(11)
+    K, N = (7168, 512) if epi in ("none", "glu") else (512, 7168)
+    # (more than one tile for a CTA or pair: the checkpoint warp then waits for most of a tile's 56 blocks)
+    counts = [9000, 11000] if epi == "glu_bwd" else [3000, 4100]
+    r, off = _routing(counts)
+    M = int(off[-1])
+    codes = lambda *n: (torch.randint(0, 0x70, n, generator=g, device=DEV, dtype=torch.int16).to(torch.uint8)     # noqa: E731
+                        .view(torch.float8_e4m3fn))
+    a = moeq.Fp8Rows(codes(M, 7168), torch.ones((56, M), device=DEV))
+    w = moeq.Fp8WeightT(codes(2, N, K), torch.full((2, -(-N // 128), -(-K // 128)), 1e-3, device=DEV))
+    ck = moeq.Fp8Rows(codes(M, 2 * K), torch.full((2 * K // 32, M), 120, dtype=torch.uint8, device=DEV)) if epi == "glu_bwd" else None
+
+    def run():
+        if epi == "none":
+            return [moeq.moe_grouped_fp8_gemm_fwd(a, w, r)]
+        if epi == "glu":
+            h, s = moeq.moe_grouped_fp8_gemm_fwd(a, w, r, moeq.EPI_SWIGLU, save_gu=True)
+            return [h.q.view(torch.uint8), h.scales, s.q.view(torch.uint8), s.scales]
+        if epi == "bwd":
+            return [moeq.moe_grouped_fp8_gemm_bwd_dx(a, w, r)]
+        d = moeq.moe_grouped_fp8_gemm_bwd_dx(a, w, r, moeq.EPI_SWIGLU_BWD, saved=ck)
+        return [d.q.view(torch.uint8), d.scales]
+    want = [t.clone() for t in run()]
+    assert moeq.moe_get_device_error() == moeq.DEVERR_NONE
+    for budget in (1, 3000, 6000, 12000, 25000, 50000, 200000):
+        try:
+            moeq.moe_test_set_wait_budget(budget)
+            got = run()
+            code = moeq.moe_get_device_error()
+        finally:
+            moeq.moe_test_set_wait_budget(0)
+        assert code in (moeq.DEVERR_NONE, moeq.DEVERR_WAIT_TIMEOUT)
+        if code == moeq.DEVERR_NONE:
+            assert all(torch.equal(x, y) for x, y in zip(got, want)), budget
+        again = run()
+        assert moeq.moe_get_device_error() == moeq.DEVERR_NONE
+        assert all(torch.equal(x, y) for x, y in zip(again, want)), budget
