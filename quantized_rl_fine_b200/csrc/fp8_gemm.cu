@@ -513,6 +513,14 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
         }
       }
       sts32(fills_at, fills);
+      if constexpr (PAIR) {
+        // The even CTA's commits arrive here too, after the last stages as well:
+        // the CTA stays until they have.
+        for (int i = 0; i < S && ok && rank == 1; ++i) {
+          ok = mbar_wait8<PAIR>(empty(st), ph ^ 1u, abort_at);
+          if (++st == S) { st = 0; ph ^= 1u; }
+        }
+      }
     }
     __syncwarp();
   } else if (warp == 1 && rank == 0) {
@@ -912,6 +920,8 @@ grouped_fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
   // and write both CTAs, have drained and both epilogues are done.
   if constexpr (PAIR) cluster_sync_all(); else __syncthreads();
   tc_fence_after();
+  // (the last of the commits that arrive in a pair's odd CTA)
+  if (rank == 1 && threadIdx.x == 0) mbar_drain(drain_bar, 0);
   if (*abort_flag) {
     // A wait has run out, in this CTA or in the pair's other one, and every role
     // has stopped, each where it was: copies may be in flight for which nobody

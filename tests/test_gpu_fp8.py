@@ -552,3 +552,23 @@ def test_products_stopped_anywhere_leave_the_next_call_clean(form, epi, monkeypa
         again = run()
         assert moeq.moe_get_device_error() == moeq.DEVERR_NONE
         assert all(torch.equal(x, y) for x, y in zip(again, want)), budget
+
+
+@pytest.mark.parametrize("blocks", [1, 2, 3, 4, 5, 9])
+def test_pairs_leave_no_arrival_behind(blocks, monkeypatch):
+    """Pairs of fewer, as many and more reduction blocks than stages, each followed at once by products of the other
+    forms on the same SMs, whose barriers lie where a late arrival of the pair would go."""
+    g = torch.Generator().manual_seed(blocks)
+    K, N = 128 * blocks, 512
+    r, _ = _routing([700, 0, 900])
+    a, _ = _rows(g, 1600, K)
+    w, _ = _weight(g, 3, N, K)
+    monkeypatch.setenv("MOEQ_F8FORM", "0")
+    want = moeq.moe_grouped_fp8_gemm_fwd(a, w, r).clone()
+    got = []
+    for i in range(60):
+        for form in ("1", "1", "023"[i % 3]):
+            monkeypatch.setenv("MOEQ_F8FORM", form)
+            got.append(moeq.moe_grouped_fp8_gemm_fwd(a, w, r))
+    assert all(torch.equal(y, want) for y in got)
+    assert moeq.moe_get_device_error() == 0
