@@ -403,7 +403,7 @@ moe_status moe_combine_bwd(const void* dy, const void* rows, const int32_t* inv_
 typedef struct moe_fp8_weight {
   const void* q;        /* device, e4m3 [E][N][K] */
   const float* scales;  /* device, fp32 [E][ceil(N/128)][ceil(K/128)] */
-  int32_t E, N, K;      /* N % 16 == 0, K % 16 == 0, 1 <= E <= 1024 */
+  int32_t E, N, K;      /* N % 16 == 0, K % 16 == 0, N and K below 2^30, 1 <= E <= 1024 */
 } moe_fp8_weight;
 
 /* Scale blocks of moe_dequantize_fp8_rows. */
@@ -438,7 +438,7 @@ moe_status moe_dequantize_fp8_rows(const void* q, const void* scales, int64_t M,
  * the blocks in fp32, in ascending b, so a row's bits do not depend on the
  * rest of the batch).
  *  a, a_scales  FP8 rows [M][K] in expert order (moe_quantize_fp8_rows).
- *  g            groups, g->E == w->E, off[E] == M.
+ *  g            groups, g->E == w->E, off[E] == M; 1 <= M <= 2^31 - 512.
  *  epi   MOE_EPI_NONE: out bf16 [M][N]; out_scales, saved and saved_scales NULL.
  *        MOE_EPI_SWIGLU (N % 256 == 0; rows 0..N/2-1 of W[e] are the gate):
  *        out, out_scales = FP8 rows of silu(acc[:, :N/2]) * acc[:, N/2:], the

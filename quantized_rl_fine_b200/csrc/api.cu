@@ -377,6 +377,9 @@ moe_status check_fp8_weight(const moe_fp8_weight* w) {
   if (!aligned16(w->q) || !aligned16(w->scales)) return MOE_ERR_MISALIGNED;
   if (w->E < 1 || w->E > 1024 || w->N < 1 || w->K < 1) return MOE_ERR_INVALID_ARG;
   if (w->K % 16 != 0 || w->N % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  // The kernel's feature indices (up to a tile past the last, and 2K in the
+  // SwiGLU backward) are 32-bit.
+  if (w->N >= (1 << 30) || w->K >= (1 << 30)) return MOE_ERR_UNSUPPORTED;
   // a tensor-map stride is below 2^40 bytes
   if (static_cast<int64_t>(w->N) * w->K >= (int64_t(1) << 40)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
@@ -593,6 +596,7 @@ moe_status check_fp8_call(const void* rows, const float* row_scales, int64_t M, 
   moe_status st = check_fp8_weight(w);
   if (st != MOE_OK) return st;
   if (M < 1 || M >= (int64_t(1) << 31)) return MOE_ERR_INVALID_ARG;
+  if (M > (int64_t(1) << 31) - 512) return MOE_ERR_UNSUPPORTED;   // 32-bit rows, up to a tile past the last
   if ((st = check_groups(g, w->E)) != MOE_OK) return st;
   if (!rows || !row_scales || !out) return MOE_ERR_INVALID_ARG;
   if (!aligned16(rows) || !aligned16(row_scales) || !aligned16(out)) return MOE_ERR_MISALIGNED;

@@ -175,6 +175,25 @@ def test_fp8_refusals(L):
     assert gemm(True, epi=2, os=P, sv=P, ss=P, K=528) == 3 and gemm(True, epi=2, os=P, sv=P, ss=P + 4) == 2
 
 
+def test_fp8_products_refuse_sizes_past_their_32_bit_indices(L):
+    """Up to a tile past the last row or feature, and 2K in the SwiGLU backward, is indexed with 32 bits."""
+    def gemm(bwd, M, N, K, epi=0):
+        w, gr = moeq.Fp8WeightC(P, P, 1, N, K), moeq.GroupsC(P, P, P, P, P, 1)
+        f = L.moe_grouped_fp8_gemm_bwd_dx if bwd else L.moe_grouped_fp8_gemm_fwd
+        if bwd:
+            return f(P, P, M, ctypes.byref(w), ctypes.byref(gr), epi, P if epi else None, P if epi else None, P, P if epi else None, None)
+        return f(P, P, M, ctypes.byref(w), ctypes.byref(gr), epi, P, P if epi else None, None, None, None)
+    top = 1 << 30
+    for M in ((1 << 31) - 1, (1 << 31) - 128, (1 << 31) - 511):
+        for bwd in (False, True):
+            assert gemm(bwd, M, 16, 16) == 3
+    for n in (top, 2 * top - 256):
+        for bwd, epi in ((False, 0), (True, 0), (False, 1)):
+            assert gemm(bwd, 64, n, 16, epi) == 3
+        for bwd, epi in ((False, 0), (True, 0), (True, 2)):
+            assert gemm(bwd, 64, 16, n, epi) == 3
+
+
 def test_bindings_refuse_on_the_host():
     lg = torch.zeros((4, 8))
     spec = moeq.RouterSpec()
