@@ -146,14 +146,14 @@ cudaError_t launch_quantize_fp8_rows(const void* x, int T, int64_t K, const int3
   // k rows (4096 x 7168 to 8 rows: 52 us, 73 with a warp per token).
   const int tpb = K <= 512 || (T >= 4096 && k == 1) ? 8 : 1;
   auto kern = tpb == 8 ? quantize_fp8_kernel<8> : quantize_fp8_kernel<1>;
-  return launch_pdl(kern, dim3((T + tpb - 1) / tpb), dim3(256), 0, s, static_cast<const uint4*>(x), T, K,
+  return launch_pdl(kern, dim3(blocks_for(T, tpb)), dim3(256), 0, s, static_cast<const uint4*>(x), T, K,
                     inv_perm, k, T * k, static_cast<uint8_t*>(q), scales);
 }
 
 cudaError_t launch_dequantize_fp8_rows(const void* q, const void* scales, int M, int64_t K, int fmt,
                                        void* out, cudaStream_t s) {
   const int64_t cols = (K / 8 + 127) / 128;
-  const dim3 grid((M + 7) / 8, static_cast<unsigned>(std::min<int64_t>(cols, 65535)));
+  const dim3 grid(blocks_for(M, 8), static_cast<unsigned>(std::min<int64_t>(cols, 65535)));
   auto kern = fmt == MOE_FP8_BLOCK128_F32 ? dequantize_fp8_kernel<MOE_FP8_BLOCK128_F32>
                                           : dequantize_fp8_kernel<MOE_FP8_BLOCK32_E8M0>;
   return launch_pdl(kern, grid, dim3(256), 0, s, static_cast<const uint8_t*>(q), scales, M, K,

@@ -8,6 +8,9 @@
 
 namespace moeq {
 
+// ceil(n / per) for any count n of tokens or rows (n + per - 1 may not fit 32 bits).
+inline unsigned blocks_for(int64_t n, int per) { return static_cast<unsigned>((n + per - 1) / per); }
+
 int route_num_blocks(int64_t T);
 // True when a routing launch takes the single-pass tail (no per-block
 // histograms, so no scratch memory).

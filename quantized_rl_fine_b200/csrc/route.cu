@@ -485,7 +485,6 @@ cudaError_t launch_route_tables(const void* x, int T, int E, int k, int64_t d, i
                                 int32_t* num_active, int32_t* chunk_offsets, int32_t* num_chunks,
                                 int32_t* perm_token, int32_t* inv_perm, void* x_perm,
                                 int32_t* block_counts, cudaStream_t s) {
-  const int W = (T + 31) / 32;
   const bool small = route_single_pass(T, E);
   const int nblk = route_num_blocks(T);
   cudaError_t err;
@@ -493,6 +492,7 @@ cudaError_t launch_route_tables(const void* x, int T, int E, int k, int64_t d, i
     int sm_count = 0;
     err = route_prepare_device(&sm_count);
     if (err != cudaSuccess) return err;
+    const int W = (T + 31) / 32;
     const size_t tsm = 2 * static_cast<size_t>(W + 1) * E * sizeof(uint32_t);
     // With x, one block per SM (at least enough for kTailRowsPerBlock rows
     // each) shares the row copy; without it one block does the tail alone.
@@ -530,7 +530,7 @@ cudaError_t launch_route_tables(const void* x, int T, int E, int k, int64_t d, i
                      static_cast<const int32_t*>(offsets), T, E, k, perm_token, inv_perm);
   }
   if (err != cudaSuccess || x == nullptr) return err;
-  return launch_pdl(permute_rows_kernel, dim3((T + 7) / 8), dim3(256), 0, s,
+  return launch_pdl(permute_rows_kernel, dim3(blocks_for(T, 8)), dim3(256), 0, s,
                     static_cast<const int32_t*>(inv_perm), T, k, static_cast<const uint4*>(x),
                     static_cast<uint4*>(x_perm), d / 8);
 }

@@ -663,7 +663,7 @@ cudaError_t launch_route_scored(const float* logits, const float* bias, const vo
   const bool small = route_single_pass(T, E);
   if (!small && block_counts == nullptr) return cudaErrorInvalidValue;
   const int tpb = small ? fit : route_tokens_per_block();
-  const int nblk = (T + tpb - 1) / tpb;
+  const int nblk = static_cast<int>(blocks_for(T, tpb));
   int32_t* hist_out = small ? nullptr : block_counts;
   // Two blocks (a cluster, one token a warp instead of two) per histogram while
   // all of them can run at once, which halves the selection's share; above
@@ -689,7 +689,7 @@ cudaError_t launch_route_scored(const float* logits, const float* bias, const vo
 cudaError_t launch_route_scored_bwd(const float* d_gates, const float* gates, const float* logits,
                                     const int32_t* topk_idx, int T, int E, int k,
                                     const moe_router& rt, float* d_logits, cudaStream_t s) {
-  return launch_pdl(route_scored_bwd_kernel, dim3((T + kBwdWarps - 1) / kBwdWarps),
+  return launch_pdl(route_scored_bwd_kernel, dim3(blocks_for(T, kBwdWarps)),
                     dim3(kBwdWarps * 32), sizeof(float) * kBwdWarps * E, s, d_gates, gates, logits, topk_idx,
                     T, E, k, rt, d_logits);
 }
