@@ -124,8 +124,8 @@ ep_regroup_kernel(const int32_t* __restrict__ counts, int W, int E_loc, int R,
     int arun = block_inclusive_scan(na, warp_tot, &atot) - na;
     for (int e = tid * per_e; e < min(E_loc, (tid + 1) * per_e); ++e)
       if (exp_off[e + 1] > exp_off[e]) active[arun++] = e;
-    const int nch = (atot + chunk_size - 1) / chunk_size;
-    for (int c = tid; c <= nch; c += kEpThreads) chunk_offsets[c] = min(c * chunk_size, atot);
+    const int nch = atot / chunk_size + (atot % chunk_size != 0 ? 1 : 0);   // (chunk_size may be any positive number)
+    for (int c = tid; c <= nch; c += kEpThreads) chunk_offsets[c] = c < nch ? c * chunk_size : atot;
     if (tid == 0) {
       *num_active = atot;
       *num_chunks = nch;

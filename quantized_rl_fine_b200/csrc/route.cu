@@ -176,12 +176,12 @@ __device__ int scan_experts(int cnt, int E, int chunk_size, int32_t* __restrict_
   }
   if (e == E - 1) offsets[E] = incl_c;
   const int A = ws_act[(E - 1) >> 5];   // inclusive total of the last warp holding an expert
-  const int nch = (A + chunk_size - 1) / chunk_size;
+  const int nch = A / chunk_size + (A % chunk_size != 0 ? 1 : 0);   // (chunk_size may be any positive number)
   if (e == 0) {
     *num_active = A;
     *num_chunks = nch;
   }
-  for (int c = e; c <= nch; c += blockDim.x) chunk_offsets[c] = min(c * chunk_size, A);
+  for (int c = e; c <= nch; c += blockDim.x) chunk_offsets[c] = c < nch ? c * chunk_size : A;
   return incl_c - cnt;
 }
 

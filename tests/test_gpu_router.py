@@ -431,3 +431,20 @@ def test_near_ties_around_the_last_of_32_places(E, groups, score, k):
     _check(logits, k, spec, bias)
     bias[bias > 2.2] = 0.0                             # 20 ahead
     _check(logits, k, spec, bias)
+
+
+@pytest.mark.parametrize("chunk", [1, 7, 8, 1 << 20, (1 << 31) - 8, (1 << 31) - 1])
+@pytest.mark.parametrize("T", [20, 200, 1500])
+def test_chunks_of_any_size(T, chunk):
+    """The chunk table for chunk sizes up to the type's largest, on each path to the tables."""
+    g = torch.Generator().manual_seed(T)
+    logits = torch.randn((T, 24), generator=g)
+    _check(logits, 3, _spec(), chunk=chunk)
+    r = moeq.moe_route_permute(logits.to(DEV), None, 3, chunk)
+    s = moeq.moe_route_scored(logits.to(DEV), None, 3, chunk, _spec())
+    n = int(r.num_chunks.item())
+    assert n == s.num_chunks.item() and torch.equal(r.chunk_offsets[:n + 1], s.chunk_offsets[:n + 1])
+    counts = (r.expert_offsets[1:] - r.expert_offsets[:-1]).view(1, 24).contiguous()
+    rows = torch.zeros((3 * T, 8), dtype=torch.bfloat16, device=DEV)
+    _, local = moeq.moe_ep_regroup(counts, rows, 0, chunk)
+    assert local.num_chunks.item() == n and torch.equal(local.chunk_offsets[:n + 1], r.chunk_offsets[:n + 1])
