@@ -94,12 +94,44 @@ quantize_fp8_kernel(const uint4* __restrict__ x, int T, int64_t K, const int32_t
   }
 }
 
+// BF16 of the exact product of an e4m3 value and any FP32 scale, rounded once.
+// It has up to 28 bits; their rounding to FP32 can end on a halfway point
+// between two BF16 values, and then the exact product (in 64 bits) decides.
+__device__ __forceinline__ uint32_t bf16_of_scaled(float q, float s) {
+  float p = q * s;
+  const uint32_t b = __float_as_uint(p);
+  if ((b & 0xffffu) == 0x8000u) {
+    const double rest = static_cast<double>(q) * s - p;
+    if (rest != 0.0) p = __uint_as_float((rest > 0.0) == (p > 0.0f) ? b + 1u : b - 1u);
+  }
+  return pack_bf16x2(p, 0.0f);
+}
+
+// Eight of them; the halfway points are looked for in all eight together.
+__device__ __forceinline__ uint4 bf16_of_scaled8(const float (&q)[8], float s) {
+  float p[8];
+  uint32_t nearest = 0xffffffffu;             // smallest distance of a product's low half from 0x8000
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    p[i] = q[i] * s;
+    nearest = min(nearest, (__float_as_uint(p[i]) & 0xffffu) ^ 0x8000u);
+  }
+  if (nearest == 0u) {
+    uint32_t h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = bf16_of_scaled(q[i], s);
+    return make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+  }
+  return make_uint4(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]), pack_bf16x2(p[6], p[7]));
+}
+
 // Blocks of 8 rows x 1024 elements, one row a warp: the rows' scales of a block
 // column lie next to each other and share their memory sectors. Eight elements
 // a lane and step, so that both the loads (8 bytes) and the stores (16) of a
 // warp are contiguous: 16 elements a lane, two stores 32 bytes apart, wrote
 // every sector in halves (32768 x 4096: 83 us). Bound: DRAM; 32768 x 4096 with
-// 1 x 32 blocks 66 us, 6.2 TB/s.
+// 1 x 32 blocks 66 us, 6.2 TB/s, and the same with FP32 scales (64 without the
+// look for halfway points).
 template <int FMT>
 __global__ void __launch_bounds__(256)
 dequantize_fp8_kernel(const uint8_t* __restrict__ q, const void* __restrict__ scales, int M, int64_t K,
@@ -129,9 +161,15 @@ dequantize_fp8_kernel(const uint8_t* __restrict__ q, const void* __restrict__ sc
       if (un >= units) continue;
       const float2 a = e4m3x2_to_float2(v[i].x), b = e4m3x2_to_float2(v[i].x >> 16);
       const float2 c = e4m3x2_to_float2(v[i].y), d = e4m3x2_to_float2(v[i].y >> 16);
-      __stcs(reinterpret_cast<uint4*>(out + m * K) + un,
-             make_uint4(pack_bf16x2(a.x * s[i], a.y * s[i]), pack_bf16x2(b.x * s[i], b.y * s[i]),
-                        pack_bf16x2(c.x * s[i], c.y * s[i]), pack_bf16x2(d.x * s[i], d.y * s[i])));
+      uint4 o;
+      if constexpr (FMT == MOE_FP8_BLOCK128_F32) {
+        const float f[8] = {a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+        o = bf16_of_scaled8(f, s[i]);
+      } else {                                // (a power of two: the FP32 product is exact)
+        o = make_uint4(pack_bf16x2(a.x * s[i], a.y * s[i]), pack_bf16x2(b.x * s[i], b.y * s[i]),
+                       pack_bf16x2(c.x * s[i], c.y * s[i]), pack_bf16x2(d.x * s[i], d.y * s[i]));
+      }
+      __stcs(reinterpret_cast<uint4*>(out + m * K) + un, o);
     }
   }
 }

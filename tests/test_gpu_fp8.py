@@ -572,3 +572,34 @@ def test_pairs_leave_no_arrival_behind(blocks, monkeypatch):
             got.append(moeq.moe_grouped_fp8_gemm_fwd(a, w, r))
     assert all(torch.equal(y, want) for y in got)
     assert moeq.moe_get_device_error() == 0
+
+
+# ----------------------------------------------------------------------------- any FP32 scale
+
+def _bf16_round(v):
+    """float64 to the nearest BF16 value (ties to even, subnormals, overflow), as float64."""
+    with np.errstate(over="ignore", invalid="ignore"):
+        _, e = np.frexp(v)
+        step = np.ldexp(1.0, np.maximum(e - 8, -133))
+        r = np.rint(v / step) * step
+        return np.where(np.abs(r) > (2.0 - 2.0 ** -7) * 2.0 ** 127, np.copysign(np.inf, r), r)
+
+
+def test_dequantize_rounds_once_for_any_scale():
+    """q * scale has up to 28 significant bits (exact in float64). Scales are random, and such that some code's
+    product lies at a halfway point between BF16 values or next to it, also among subnormals and near the largest."""
+    g = np.random.RandomState(11)
+    vals = O8.e4m3_values()
+    pos = vals[(vals > 0)]
+    tie = (1 + (2 * g.randint(0, 128, 6000) + 1) / 256.0) * 2.0 ** g.randint(-140, 127, 6000)
+    near = (tie / g.choice(pos, 6000)).astype(np.float32)
+    s = np.concatenate([[1.6541667], near, np.nextafter(near, np.float32(np.inf)), np.nextafter(near, np.float32(0)),
+                        2.0 ** g.uniform(-149, 127.9, 6000), 2.0 ** np.arange(-126, 127)]).astype(np.float32)
+    M = len(s)
+    codes = np.tile(np.arange(256, dtype=np.uint8), (M, 1))
+    sc = np.stack([s, -s])                                  # the negative half of the codes with a negative scale
+    got = f64(moeq.moe_dequantize_fp8_rows(moeq.Fp8Rows(_fp8(codes), torch.from_numpy(sc).to(DEV))))
+    want = vals[None, :] * np.repeat(sc.T.astype(np.float64), 128, 1)
+    nan = np.isnan(want)
+    assert np.array_equal(np.isnan(got), nan)
+    assert np.array_equal(got[~nan], _bf16_round(want)[~nan])
