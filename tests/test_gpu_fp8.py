@@ -603,3 +603,53 @@ def test_dequantize_rounds_once_for_any_scale():
     nan = np.isnan(want)
     assert np.array_equal(np.isnan(got), nan)
     assert np.array_equal(got[~nan], _bf16_round(want)[~nan])
+
+
+def test_calls_from_several_host_threads_at_once():
+    """Routing of several sizes and FP8 products of all four tile forms, each thread on a stream of its own: every
+    output of every iteration, and an error in a thread is an error of the test."""
+    from concurrent.futures import ThreadPoolExecutor
+    g = torch.Generator().manual_seed(8)
+    jobs = []
+    for T, E, groups in ((20, 384, 8), (3000, 256, 8), (700, 1024, 32), (1, 64, 4)):
+        lg, b = torch.randn((T, E), generator=g).to(DEV), (0.1 * torch.randn(E, generator=g)).to(DEV)
+        sp = moeq.RouterSpec(score="sigmoid", groups=groups, topk_groups=2, group_top=2)
+        dg = torch.randn((T, 4), generator=g).to(DEV)
+
+        def route(stream, lg=lg, b=b, sp=sp, dg=dg):
+            r = moeq.moe_route_scored(lg, None, 4, 8, sp, bias=b, stream=stream)
+            n = int(r.num_active.item())
+            return (r.topk_idx, r.gates, r.expert_offsets, r.active[:n], r.num_active, r.num_chunks, r.perm_token, r.inv_perm,
+                    moeq.moe_route_scored_bwd(dg, lg, r, sp, stream=stream))
+        jobs.append(route)
+    K, f = 272, 128
+    w, wd = _weight(g, 2, 2 * f, K)[0], _weight(g, 2, K, f)[0]
+    for counts in ([9, 20], [30, 40], [100, 200], [700, 600]):              # 32, 64 and 128 rows a tile, pairs
+        r, off = _routing(counts)
+        x = torch.randn((int(off[-1]), K), generator=g).to(torch.bfloat16).to(DEV)
+
+        def product(stream, r=r, x=x):
+            a = moeq.moe_quantize_fp8_rows(x, r, stream=stream)
+            h, s = moeq.moe_grouped_fp8_gemm_fwd(a, w, r, moeq.EPI_SWIGLU, save_gu=True, stream=stream)
+            y = moeq.moe_grouped_fp8_gemm_fwd(h, wd, r, stream=stream)
+            d = moeq.moe_grouped_fp8_gemm_bwd_dx(moeq.moe_quantize_fp8_rows(y, stream=stream), wd, r, moeq.EPI_SWIGLU_BWD,
+                                                 saved=s, stream=stream)
+            return (h.q.view(torch.uint8), h.scales, s.q.view(torch.uint8), s.scales, y, d.q.view(torch.uint8), d.scales)
+        jobs.append(product)
+    want = [[t.clone() for t in job(None)] for job in jobs]
+    torch.cuda.synchronize()
+
+    def work(i):
+        done = 0
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                got = jobs[i](s)
+                s.synchronize()
+                for n, (a, b) in enumerate(zip(got, want[i])):
+                    assert torch.equal(a, b), (i, n)
+                done += 1
+        return done
+    with ThreadPoolExecutor(len(jobs)) as pool:
+        assert [t.result() for t in [pool.submit(work, i) for i in range(len(jobs))]] == [20] * len(jobs)
+    assert moeq.moe_get_device_error() == 0
