@@ -105,18 +105,19 @@ def expert_compute(rows: torch.Tensor, recv_counts: torch.Tensor, w_gu: QWeightT
     """Phase 2 on the owner: received rows (source-major) -> local expert-major
     -> gate/up + SwiGLU -> down -> back to source-major order."""
     layer.check_weights(w_gu, w_d)
+    if isinstance(w_gu, M.Fp8WeightT) and adapter is not None:
+        raise ValueError("FP8 experts take no adapter")
     if rows.shape[0] == 0:                      # no token chose this rank's experts
         return rows.new_empty((0, w_d.N))
-    xl, groups = M.moe_ep_regroup(recv_counts, rows, 0, chunk_size)
-    if isinstance(w_gu, M.Fp8WeightT):
-        if adapter is not None:
-            raise ValueError("FP8 experts take no adapter")
-        h, _ = M.moe_grouped_fp8_gemm_fwd(M.moe_quantize_fp8_rows(xl), w_gu, groups, M.EPI_SWIGLU)
-        yl = M.moe_grouped_fp8_gemm_fwd(h, w_d, groups)
-    else:
-        h, _ = M.moe_grouped_qgemm_fwd(xl, w_gu, groups, M.EPI_SWIGLU, adapter=adapter)
-        yl = M.moe_grouped_qgemm_fwd(h, w_d, groups, M.EPI_NONE)
-    return M.moe_ep_regroup(recv_counts, yl, 1)
+    with M._on(rows.device, None):              # every call on the rows' device
+        xl, groups = M.moe_ep_regroup(recv_counts, rows, 0, chunk_size)
+        if isinstance(w_gu, M.Fp8WeightT):
+            h, _ = M.moe_grouped_fp8_gemm_fwd(M.moe_quantize_fp8_rows(xl), w_gu, groups, M.EPI_SWIGLU)
+            yl = M.moe_grouped_fp8_gemm_fwd(h, w_d, groups)
+        else:
+            h, _ = M.moe_grouped_qgemm_fwd(xl, w_gu, groups, M.EPI_SWIGLU, adapter=adapter)
+            yl = M.moe_grouped_qgemm_fwd(h, w_d, groups, M.EPI_NONE)
+        return M.moe_ep_regroup(recv_counts, yl, 1)
 
 
 def combine(dsp: Dispatch, y_perm: torch.Tensor, T: int) -> torch.Tensor:

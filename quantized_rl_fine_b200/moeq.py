@@ -384,6 +384,10 @@ _HERE = contextlib.nullcontext()
 
 def _on(device, stream):
     """The tensors' device, and `stream` (if any) as its current stream."""
+    if device.type != "cuda":
+        raise ValueError("libmoeq takes CUDA tensors only")
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream: of {stream.device}, but the tensors are on {device}")
     if stream is None and device.index == torch.cuda.current_device():
         return _HERE
     return _switch(device, stream)

@@ -163,3 +163,46 @@ def test_expert_parallel_phases_with_fp8_experts():
     got = torch.cat([ep.combine(dsp[s], torch.cat(back[s]), T) for s in range(W)])
     assert moeq.moe_get_device_error() == 0
     assert torch.equal(got, want)
+
+
+def _pool_stream(t):
+    """The stream whose memory pool holds the tensor."""
+    p = t.data_ptr()
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= p < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not in a pool")
+
+
+@pytest.mark.parametrize("kind", ["fp8", "int4", "int4_adapter", "up"])
+def test_a_step_on_another_stream_lives_in_that_streams_memory(kind):
+    """Whatever a step on a given stream writes comes from that stream's pool: memory of the current stream's
+    pool may still be in use there. And the results are those of the current stream."""
+    E, k, d, f, T = 4, 2, 128, 128, 50
+    if kind == "fp8":
+        g, x, dy, wg, wd = _fp8_layer(E, d, f, T, 3)
+        lg, R = torch.randn((T, E), generator=g).to(DEV), None
+    else:
+        cfg = MoEConfig("t", E=E, k=k, d=d, f=f, T=T, fmt="int4", swiglu=True, logits="normal", adapter=True, train=True, seed=6)
+        wl = synth.make_workload(cfg, "cpu")
+        wg, wd = wl["w_gu"].to(DEV), wl["w_d"].to(DEV)
+        x, lg, dy, R = (wl[n].to(DEV) for n in ("x", "logits", "dy", "adapter"))
+        R = R if kind == "int4_adapter" else None
+
+    def step(stream=None):
+        if kind == "up":
+            st = layer.up_projection(x, lg, wg, k, 8, stream=stream)
+            return dict(out=st["out"], a=st["a"], perm=st["routing"].perm_token)
+        st = layer.forward(x, lg, wg, wd, k, 8, adapter=R, train=True, stream=stream, router=moeq.RouterSpec())
+        bw = layer.backward(st, dy, wg, wd, adapter=R, stream=stream)
+        outs = {n: t for n, t in {**st, **bw}.items() if isinstance(t, torch.Tensor) and n not in ("x", "logits", "a", "a_rows")}
+        return dict(outs, perm=st["routing"].perm_token)
+    want = {n: t.clone() for n, t in step().items()}
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = step(side)
+    side.synchronize()
+    assert moeq.moe_get_device_error() == 0
+    for n, t in want.items():
+        assert torch.equal(got[n], t), n
+        assert _pool_stream(got[n]) == side.cuda_stream, n

@@ -222,3 +222,41 @@ def test_bindings_refuse_on_the_host():
             layer.backward(dict(routing=None), lg, *pair)
         with pytest.raises(ValueError, match="both"):
             ep.expert_compute(lg, lg, *pair, 8)
+
+
+def test_streams_and_devices_of_a_step(monkeypatch):
+    """Without a GPU: a stream of another device than the tensors' is refused, and a step enters the tensors'
+    device and the given stream before its first call."""
+    class Stream:
+        def __init__(self, index):
+            self.device = torch.device("cuda", index)
+    with pytest.raises(ValueError, match="stream"):
+        moeq._on(torch.device("cuda", 0), Stream(1))
+    with pytest.raises(ValueError, match="CUDA"):
+        moeq._on(torch.device("cpu"), None)
+
+    class Entered(Exception):
+        pass
+    seen = []
+
+    def on(device, stream):
+        seen.append((device, stream))
+        raise Entered
+    monkeypatch.setattr(moeq, "_on", on)
+    lg = torch.zeros((4, 8))
+    fp8 = moeq.Fp8WeightT(torch.zeros((2, 16, 16), dtype=torch.float8_e4m3fn), torch.ones((2, 1, 1)))
+    four = synth.QWeightT("int4", torch.zeros((2, 64, 32), dtype=torch.uint8), torch.ones((2, 2, 64), dtype=torch.bfloat16))
+    s = Stream(0)
+    state = dict(routing=None, saved_gu=lg)
+    for w in (fp8, four):
+        for call in (lambda: layer.forward(lg, lg, w, w, 2, 8, stream=s), lambda: layer.backward(state, lg, w, w, stream=s)):
+            with pytest.raises(Entered):
+                call()
+    for call in (lambda: layer.route(lg, lg, 2, 8, stream=s), lambda: layer.route(lg, lg, 2, 8, moeq.RouterSpec(), stream=s),
+                 lambda: layer.up_projection(lg, lg, four, 2, 8, stream=s)):
+        with pytest.raises(Entered):
+            call()
+    assert seen == [(lg.device, s)] * 7
+    with pytest.raises(Entered):
+        ep.expert_compute(lg, lg, fp8, fp8, 8)
+    assert seen[-1] == (lg.device, None)
