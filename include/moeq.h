@@ -337,10 +337,13 @@ typedef struct moe_router {
  * Equal keys and equal groups go to the lower id. Keys are compared as if in
  * 64 bits (without a bias, by the logits themselves, which have the same
  * order). An expert whose logit is NaN or -inf, or whose key is NaN or -inf,
- * is masked: its score is 0 and it is chosen only when fewer than k experts of
- * the kept groups are left (in ascending id, gate 0); a masked key adds
- * nothing to its group's score, and a group of masked experts ranks last. A token whose selected scores sum
- * to 0 gets gates 0.
+ * is masked: it is chosen only when fewer than k experts of the kept groups
+ * are left (in ascending id), its gate is then 0 and its score counts as 0 in
+ * the sum over the selected; a masked key adds nothing to its group's score,
+ * and a group of masked experts ranks last. The softmax runs over the experts
+ * whose logit is neither NaN nor -inf, those masked by their key alone (a bias
+ * of -inf) among them: the bias changes no score. A token whose selected
+ * scores sum to 0 gets gates 0.
  * The k experts of a token are always distinct. All other arguments, outputs
  * and limits are those of moe_route_permute, the workspace size included.
  */
@@ -366,7 +369,10 @@ moe_status moe_route_scored(const float* logits, const float* bias, const void* 
  *   ds_j = c * d_gates_j, or with renorm c * (d_gates_j - sum_i d_gates_i s_i / S) / S
  *   sigmoid: d_logits_j = ds_j s_j (1 - s_j), other experts 0
  *   softmax: d_logits_e = s_e (ds_e - sum_j ds_j s_j)  (ds_e = 0 when not selected)
- * Masked experts get 0, and so does a token with S == 0. Requires T >= 1,
+ * An expert masked by its logit gets 0, and so does a token with S == 0. One
+ * masked by its key alone gets what an expert that is not selected gets, also
+ * in a slot with gate 0: nothing, or its softmax term -s_e sum_j ds_j s_j,
+ * because it is part of the denominator. Requires T >= 1,
  * 1 <= E <= 1024, 1 <= k <= min(E, 32). Only score, renorm and scale of
  * `router` are read.
  */

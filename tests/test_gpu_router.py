@@ -448,3 +448,49 @@ def test_chunks_of_any_size(T, chunk):
     rows = torch.zeros((3 * T, 8), dtype=torch.bfloat16, device=DEV)
     _, local = moeq.moe_ep_regroup(counts, rows, 0, chunk)
     assert local.num_chunks.item() == n and torch.equal(local.chunk_offsets[:n + 1], r.chunk_offsets[:n + 1])
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("scale", [1.0, 2.5])
+def test_gradient_of_experts_masked_by_the_bias(score, renorm, scale):
+    """An expert that only its key masks stays in the softmax's denominator, as in the forward: with plain softmax
+    gates its logit gets -s_e sum_j ds_j s_j like every expert that is not selected, and 0 otherwise. An expert
+    masked by its logit gets 0. Against the formula and against differences of the forward's own gates."""
+    T, E, k, h = 40, 9, 4, 2.0 ** -7
+    g = torch.Generator().manual_seed(3)
+    logits = (512 * torch.randn((T, E), generator=g)).round() / 1024          # logits +- h are exact
+    logits[:, 8] = -float("inf")
+    bias = torch.tensor([0.0, -float("inf"), 0.3, float("nan"), -float("inf"), -0.3, 0.6, 0.1, 0.2])
+    dg = torch.randn((T, k), generator=g)
+    by_key, open_ = [1, 3, 4], [0, 2, 5, 6, 7]
+    spec = _spec(score=score, renorm=renorm, scale=scale)
+
+    def gates(lg):
+        r = moeq.moe_route_scored(lg.to(DEV), None, k, 8, spec, bias=bias.to(DEV))
+        return r, f64(r.gates)
+    r, w = gates(logits)
+    idx = r.topk_idx.cpu().numpy()
+    assert set(idx.ravel().tolist()) <= set(open_)
+    got = f64(moeq.moe_route_scored_bwd(dg.to(DEV), logits.to(DEV), r, spec))
+    d = dg.numpy().astype(np.float64)
+    s = O8.scored_scores(logits.numpy(), score)
+    sel = np.take_along_axis(s, idx.astype(np.int64), 1)
+    if score == "softmax" and not renorm:
+        want = -s[:, by_key] * (scale * d * sel).sum(1, keepdims=True)
+        assert np.all(np.abs(got[:, by_key] - want) <= 256 * U * s[:, by_key] * (scale * np.abs(d) * sel).sum(1, keepdims=True))
+        assert np.abs(got[:, by_key]).max() > 0.05
+    else:
+        assert not got[:, by_key].any()
+    assert not got[:, 8].any()
+    # Differences: gates have third derivatives below 6 scale (scores above 0.2 here), so h^2 scale; each gate is
+    # off by 64 U, twice over 2 h.
+    lim = (h * h + 64 * U / h) * scale * np.abs(d).sum(1)
+    for e in range(8):
+        step = torch.zeros(E)
+        step[e] = h
+        up, down = gates(logits + step), gates(logits - step)
+        same = (up[0].topk_idx.cpu().numpy() == idx).all(1) & (down[0].topk_idx.cpu().numpy() == idx).all(1)
+        assert same.sum() > T / 2                                             # (the selection itself moves in few)
+        num = ((up[1] - down[1]) * d).sum(1) / (2 * h)
+        assert np.all(np.abs(num - got[:, e])[same] <= lim[same] + 256 * U * scale * np.abs(d).sum(1)[same])
