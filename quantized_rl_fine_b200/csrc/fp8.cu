@@ -49,7 +49,10 @@ __device__ __forceinline__ uint4 quantize16(const uint4& a, const uint4& b, floa
 // quantized once and written to its k rows (16-byte stores), which costs k
 // writes of one byte an element against k reads of two if every permuted row
 // were quantized by itself. Bound: DRAM, read once and written k times;
-// 32768 x 7168 112 us (6.3 TB/s), 4096 x 7168 to 8 rows 52 us (5.7 TB/s).
+// 32768 x 7168 111 us (6.4 TB/s), 4096 x 7168 to 8 rows 59 us (5.1 TB/s). Narrower
+// rows written to several leave part of a token's 256 threads, which cover 8192
+// elements a step, without work: 8192 x 4096 to 8 rows 66 us (5.2 TB/s), 8192 x 2048
+// 42.5 (4.0), 16384 x 1024 70 (2.5), all of 26 to 52 us at the copy rate.
 template <int TPB>
 __global__ void __launch_bounds__(256)
 quantize_fp8_kernel(const uint4* __restrict__ x, int T, int64_t K, const int32_t* __restrict__ inv_perm,
@@ -181,7 +184,8 @@ cudaError_t launch_quantize_fp8_rows(const void* x, int T, int64_t K, const int3
   // A warp per token when there are enough tokens to fill the SMs that way and
   // each is written once (32768 x 7168: 112 us, 150 with a block per token);
   // a block per token for few tokens (latency), and when a token is written to
-  // k rows (4096 x 7168 to 8 rows: 52 us, 73 with a warp per token).
+  // k rows (4096 x 7168 to 8 rows: 59 us, some 20 more with a warp per token). The
+  // latter is measured at K = 7168 only.
   const int tpb = K <= 512 || (T >= 4096 && k == 1) ? 8 : 1;
   auto kern = tpb == 8 ? quantize_fp8_kernel<8> : quantize_fp8_kernel<1>;
   return launch_pdl(kern, dim3(blocks_for(T, tpb)), dim3(256), 0, s, static_cast<const uint4*>(x), T, K,

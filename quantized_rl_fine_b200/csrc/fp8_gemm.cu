@@ -33,9 +33,11 @@
 // 1040 / 1225, with checkpoint 1078 / 1275 (its epilogue, about 2 us a tile, is
 // not overlapped: the accumulators are in registers). SwiGLU backward 607 us for
 // half the work.
-// Tried, without gain: 128-column tiles or a column split with their own barriers
-// (the time per hand-over stays), two MMA issuers, spinning waits, tensor-memory
-// loads held over the loop's back edge (the compiler cannot keep the registers).
+// Tried, without gain: two MMA issuers, spinning waits, tensor-memory loads held
+// over the loop's back edge (the compiler cannot keep the registers). 128-column
+// tiles and a column split with their own barriers gained nothing while the
+// epilogue threads loaded the scales themselves, which then bounded a block
+// whatever its width; they have not been measured since the scale warp does.
 //
 // The backward reads the same weights in place, as the MN-major B operand:
 // features contiguous, 128-byte swizzled blocks of 128 features.

@@ -22,7 +22,7 @@ struct Fp8GemmArgs {
   float* out_scales;           // e4m3 rows: [blocks][M]
   uint8_t* saved;              // checkpoint e4m3 [M][2f]: written (forward, may be NULL) or read
   uint8_t* saved_scales;       // checkpoint E8M0 [2f/32][M]
-  int32_t w_once;              // 1: weights leave L2 first (an expert's are read once)
+  int32_t w_once;              // 1: weights leave L2 first (few rows an expert)
 };
 
 // form: 0 single CTAs on 128 token rows, 1 clusters of two CTAs on 256 (grid: CTAs,

@@ -8,10 +8,10 @@
 // A token's selection is a chain of dependent warp reductions (about 2 us),
 // so what bounds it is latency: a warp per token, everything in registers,
 // three launches for many tokens and one for a decode batch. Measured, whole
-// call in a graph: 1 token of 384 experts in 8 groups with bias 8.7 us, 32
+// call in a graph: 1 token of 384 experts in 8 groups with bias 9 us, 32
 // tokens 14.5, 4096 tokens of 256 experts 21 to 25 (about 13 of it the scan of the
-// counts and the scatter), 16384 of 384 softmax without groups 39.5 (to read
-// the 25 MB of logits would take 4). FP32 keys against 64-bit keys
+// counts and the scatter; 35 for k = 32), 16384 of 384 softmax without groups 40 (to
+// read the 25 MB of logits would take 4). FP32 keys against 64-bit keys
 // throughout: 39.5 / 88 us, and for the 4096 tokens, then in half as many
 // blocks, 32.5 / 51. A token whose keys need 64 bits takes some 5 us more, and in a
 // few thousand there are some, so the bound on the FP32 keys' error counts.
@@ -527,8 +527,11 @@ route_scored_small_kernel(const float* __restrict__ logits, const float* __restr
 // row of the warp's shared memory, then the whole row of d_logits written
 // once. What belongs to the k selected scores is in 64 bits, because renorm
 // subtracts nearly equal numbers and divides by a sum that may lie below
-// FP32; the dense softmax part is in 32. Bound: DRAM, one row of logits read
-// (softmax) and one of d_logits written; 4096 x 384 takes 11 us, 6.3 MB written.
+// FP32; the dense softmax part is in 32. Bound: latency, not the one row of
+// logits read (softmax) and one of d_logits written: a warp makes up to three
+// passes over the row with 4-byte accesses, and the 64-bit exponentials keep k of
+// 32 lanes busy. 4096 x 384: softmax 10.7 us (13 MB, 2.0 at the copy rate), sigmoid
+// 5.1 (6.8 MB, 1.0), at 7 and 5 % of DRAM's throughput; 16384 x 384: 21.3 and 10.2.
 constexpr int kBwdWarps = 8;
 __global__ void __launch_bounds__(kBwdWarps * 32)
 route_scored_bwd_kernel(const float* __restrict__ d_gates, const float* __restrict__ gates,
