@@ -8,8 +8,8 @@
 // A token's selection is a chain of dependent warp reductions (about 2 us),
 // so what bounds it is latency: a warp per token, everything in registers,
 // three launches for many tokens and one for a decode batch. Measured, whole
-// call in a graph: 1 token of 384 experts in 8 groups with bias 9 us, 32
-// tokens 14.5, 4096 tokens of 256 experts 21 to 25 (about 13 of it the scan of the
+// call in a graph: 1 token of 384 experts in 8 groups with bias 9.7 us, 32
+// tokens 15, 4096 tokens of 256 experts 21 to 25 (about 13 of it the scan of the
 // counts and the scatter; 35 for k = 32), 16384 of 384 softmax without groups 40 (to
 // read the 25 MB of logits would take 4). FP32 keys against 64-bit keys
 // throughout: 39.5 / 88 us, and for the 4096 tokens, then in half as many
@@ -171,7 +171,7 @@ __device__ __forceinline__ unsigned open_groups(const Real (&gv)[NPER], Real* wr
 template <int NPER>
 __device__ __forceinline__ void select_token(const float* __restrict__ row, const float* __restrict__ bias, int E,
                                              int k, const moe_router& rt, double* wrow, int lane, float* mx_out,
-                                             double* total_out, int* my_idx_out, bool* my_open_out) {
+                                             float* total_out, int* my_idx_out, bool* my_open_out) {
   const unsigned full = 0xffffffffu;
   const bool grouped = rt.groups > 1, softmax = rt.score == MOE_SCORE_SOFTMAX;
   const uint32_t magic = group_magic(E / rt.groups);
@@ -348,7 +348,7 @@ __device__ __forceinline__ void select_token(const float* __restrict__ row, cons
         if (is_open(l[i])) z64 += (l[i] == mx) ? 1.0 : exp(static_cast<double>(l[i]) - mx);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) z64 += __shfl_xor_sync(full, z64, o);
-      *total_out = z64;
+      *total_out = static_cast<float>(z64);
     }
     unsigned long long key[NPER];
     double gv[NPER];
@@ -399,24 +399,48 @@ __device__ __forceinline__ void select_token(const float* __restrict__ row, cons
   *my_open_out = my_open && lane < k;
 }
 
-// Gate of the lane's selected expert, in FP32; where renorm divides by a sum
-// that FP32 hardly holds (sigmoids far below zero), in 64 bits.
-__device__ __forceinline__ float gate_of(const float* __restrict__ row, int idx, bool open, float mx, double total,
+// exp(v - ref) for v <= ref, to a few ulp: the rounding of the difference, up
+// to 2^-18 of the result by itself, is put back.
+__device__ __forceinline__ float exp_below(float v, float ref) {
+  if (v == ref) return 1.0f;              // (two infinities too)
+  const float d = v - ref;
+  if (!(d > -110.0f)) return 0.0f;        // below FP32's smallest
+  const float back = d - v;
+  const float rest = (v - (d - back)) - (ref + back);   // v - ref - d, exactly
+  const float s = expf(d);
+  return fmaf(s, rest, s);
+}
+
+// Gate of the lane's selected expert, in FP32. With renorm a softmax is taken
+// over the selected logits alone, which is the same quotient without the small
+// numbers (a bias or closed groups can leave only scores far below the largest);
+// sigmoids far below zero, whose quotients FP32 does not hold, are taken in 64 bits.
+__device__ __forceinline__ float gate_of(const float* __restrict__ row, int idx, bool open, float mx, float total,
                                          const moe_router& rt) {
   const unsigned full = 0xffffffffu;
   const bool softmax = rt.score == MOE_SCORE_SOFTMAX;
-  float s = 0.0f, v = 0.0f;
-  if (open) {
-    v = __ldg(row + idx);
-    s = softmax ? ((v == mx) ? 1.0f : expf(v - mx)) / static_cast<float>(total) : 1.0f / (1.0f + expf(-v));
+  const float v = open ? __ldg(row + idx) : -INFINITY;
+  float s = 0.0f;
+  if (!rt.renorm) {
+    if (open) s = softmax ? exp_below(v, mx) / total : 1.0f / (1.0f + expf(-v));
+    return rt.scale * s;
   }
-  if (!rt.renorm) return rt.scale * s;
-  float sum = s;
+  if (softmax) {
+    float top = v;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(full, sum, o);
-  if (sum > 1e-30f) return rt.scale * (s / sum);
-  double s64 = 0.0;
-  if (open) s64 = softmax ? ((v == mx) ? 1.0 : exp(static_cast<double>(v) - mx)) / total : sigmoid64(v);
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(full, top, o));
+    // (scores that are 0 in 64 bits sum to 0)
+    if (open && (top == mx || exp(static_cast<double>(top) - mx) > 0.0)) s = exp_below(v, top);
+  } else if (open) {
+    s = 1.0f / (1.0f + expf(-v));
+  }
+  if (softmax || !__any_sync(full, open && v < -64.0f)) {
+    float sum = s;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(full, sum, o);
+    return rt.scale * (sum > 0.0f ? s / sum : 0.0f);
+  }
+  const double s64 = open ? sigmoid64(v) : 0.0;
   double sum64 = s64;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum64 += __shfl_xor_sync(full, sum64, o);
@@ -447,7 +471,7 @@ route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ 
     if (t >= T) break;
     const float* row = logits + static_cast<int64_t>(t) * E;
     float mx;
-    double total;
+    float total;
     int idx;
     bool open;
     select_token<NPER>(row, bias, E, k, rt, scored_sm + warp * row_el, lane, &mx, &total, &idx,
@@ -498,7 +522,7 @@ route_scored_small_kernel(const float* __restrict__ logits, const float* __restr
   if (warp < T) {
     const float* row = logits + static_cast<int64_t>(warp) * E;
     float mx;
-    double total;
+    float total;
     int idx;
     bool open;
     select_token<NPER>(row, bias, E, k, rt, scored_sm + warp * row_el, lane, &mx, &total, &idx,

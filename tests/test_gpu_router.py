@@ -494,3 +494,30 @@ def test_gradient_of_experts_masked_by_the_bias(score, renorm, scale):
         assert same.sum() > T / 2                                             # (the selection itself moves in few)
         num = ((up[1] - down[1]) * d).sum(1) / (2 * h)
         assert np.all(np.abs(num - got[:, e])[same] <= lim[same] + 256 * U * scale * np.abs(d).sum(1)[same])
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("spread", [10.0, 30.0, 60.0])
+@pytest.mark.parametrize("groups,with_bias", [(1, False), (1, True), (8, False), (8, True)])
+def test_gates_of_scores_far_apart(score, renorm, spread, groups, with_bias):
+    """Logits over hundreds: differences with a rounding of their own, and tokens whose bias or groups leave only
+    experts with scores near and below single precision's smallest number."""
+    T, E, k = 200, 64, 8
+    g = torch.Generator().manual_seed(int(spread) + groups)
+    logits = spread * torch.randn((T, E), generator=g)
+    logits[:40] -= 40 + logits[:40].amax(1, keepdim=True)                     # sigmoids of -40 and below
+    bias = 2 * torch.randn(E, generator=g) if with_bias else None
+    _check(logits, k, _spec(score=score, renorm=renorm, groups=groups, topk_groups=max(1, groups // 4), scale=1.5), bias)
+
+
+def test_gates_of_scores_that_are_zero():
+    """A logit of +inf that the bias keeps out of the selection takes the whole softmax: the gates are 0."""
+    logits = torch.randn((20, 16), generator=torch.Generator().manual_seed(1))
+    logits[:, 3] = float("inf")
+    logits[10:, 3] = 3.0e38
+    bias = torch.zeros(16)
+    bias[3] = -10.0
+    for renorm in (False, True):
+        r, topk = _check(logits, 4, _spec(renorm=renorm), bias)
+        assert not np.any(topk == 3) and not r.gates.any()
