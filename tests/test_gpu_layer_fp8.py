@@ -206,3 +206,41 @@ def test_a_step_on_another_stream_lives_in_that_streams_memory(kind):
     for n, t in want.items():
         assert torch.equal(got[n], t), n
         assert _pool_stream(got[n]) == side.cuda_stream, n
+
+
+@pytest.mark.parametrize("kind", ["fp8", "int4"])
+def test_a_captured_step_replays_on_new_inputs(kind):
+    """Forward and backward of a layer with a scored router in one graph: replayed on other inputs it gives the bits
+    of the calls themselves, with a second graph of the same layer and eager steps in between."""
+    E, k, d, f, T = 8, 2, 128, 128, 1100
+    g, x0, dy0, wg, wd = _fp8_layer(E, d, f, T, 21)
+    if kind == "int4":
+        cfg = MoEConfig("t", E=E, k=k, d=d, f=f, T=T, fmt="int4", swiglu=True, logits="normal", adapter=False, train=True, seed=7)
+        wl = synth.make_workload(cfg, "cpu")
+        wg, wd = wl["w_gu"].to(DEV), wl["w_d"].to(DEV)
+    spec, bias = moeq.RouterSpec(score="sigmoid", groups=4, topk_groups=2, group_top=2), (0.1 * torch.randn(E, generator=g)).to(DEV)
+    sets = [(x0, torch.randn((T, E), generator=g).to(DEV), dy0)]
+    sets.append(tuple(torch.randn(t.shape, generator=g).to(t.dtype).to(DEV) for t in sets[0]))
+
+    def step(x, lg, dy):
+        st = layer.forward(x, lg, wg, wd, k, 8, train=True, router=spec, bias=bias)
+        bw = layer.backward(st, dy, wg, wd)
+        return st["y"], st["routing"].gates, bw["dx"], bw["d_logits"], bw["d_gates"]
+    want = [[t.clone() for t in step(*s)] for s in sets]
+    graphs = []
+    for _ in range(2):
+        ins = [t.clone() for t in sets[0]]
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            outs = step(*ins)
+        graphs.append((graph, ins, outs))
+    for i, (a, b) in ((0, (1, 0)), (1, (0, 1))):
+        for (graph, ins, _), s in zip(graphs, (a, b)):
+            for t, v in zip(ins, sets[s]):
+                t.copy_(v)
+            graph.replay()
+        assert all(torch.equal(p, q) for p, q in zip(step(*sets[i]), want[i]))
+        for (_, _, outs), s in zip(graphs, (a, b)):
+            assert all(torch.equal(p, q) for p, q in zip(outs, want[s]))
+    assert moeq.moe_get_device_error() == 0
